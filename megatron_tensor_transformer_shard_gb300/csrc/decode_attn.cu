@@ -249,9 +249,12 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
   int* pre = reinterpret_cast<int*>(base + C::OFF_PRE);     // [B + 1] tile prefix of the sequences
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // WIN: this is the first kernel of the call, and the one before it on the stream may write pos, so
+  // every thread waits for it before anything is read; then CTAs without a tile, which return below,
+  // are behind that kernel too, and so is whoever waits for this grid.  Otherwise the projection runs
+  // before, and the plan is formed beside its end.
+  if (WIN) ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  // The plan comes from pos (an input of the call, complete before the first
-  // kernel of the call started), so it may be read before griddepcontrol.wait.
   if (WIN) {
     if (blockIdx.x == 0)
       for (int b = threadIdx.x; b < p.B; b += blockDim.x)
@@ -306,14 +309,14 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
     if (lane == 0) {
       ptx::tma_prefetch_desc(&tm_k);
       ptx::tma_prefetch_desc(&tm_q);
-      ptx::griddep_wait();  // Q and the newest cache entries come from the previous kernel
+      if (!WIN) ptx::griddep_wait();  // Q and the newest cache entries come from the previous kernel
       int u = 0, seg = 0;
       bool ok = true;
       DecodeRuns runs{};
       for (; ok && cur.valid(); cur.next()) {
         const int s = cur.s;
         if (cur.first(x0)) {
-          if (WIN) runs = decode_runs(p.win, __ldg(p.pos + s % p.B));
+          if (WIN) runs = decode_runs(p.win, p.pos[s % p.B]);
           const int qb = seg & 1;
           if (!ptx::mbar_wait(&q_empty[qb], ((seg >> 1) & 1) ^ 1u, abort_flag, p.err, ERR_DEC_PRODUCER,
                               p.timeout_ns)) {
@@ -354,11 +357,11 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
     // while a K stage frees right after the S MMA, so K can run further ahead.
     if (lane == 0) {
       ptx::tma_prefetch_desc(&tm_v);
-      ptx::griddep_wait();
+      if (!WIN) ptx::griddep_wait();
       int u = 0;
       DecodeRuns runs{};
       for (; cur.valid(); cur.next()) {
-        if (WIN && cur.first(x0)) runs = decode_runs(p.win, __ldg(p.pos + cur.s % p.B));
+        if (WIN && cur.first(x0)) runs = decode_runs(p.win, p.pos[cur.s % p.B]);
         const int st = u % ST;
         if (!ptx::mbar_wait(&v_empty[st], ((u / ST) & 1) ^ 1u, abort_flag, p.err, ERR_DEC_PRODUCER, p.timeout_ns))
           break;
@@ -508,7 +511,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
       const int s = cur.s, sb = u & 1;
       if (s != s_cur) {
         s_cur = s;
-        if (WIN) runs = decode_runs(p.win, __ldg(p.pos + s % p.B));
+        if (WIN) runs = decode_runs(p.win, p.pos[s % p.B]);
         else len = stream_len(p.pos, s % p.B, p.L_max);
       }
       const int nvalid = WIN ? runs.valid(cur.local_tile()) : len - cur.local_tile() * BK;  // >= 1
@@ -638,8 +641,10 @@ constexpr int CMB_WARPS = 4;
 template <int NG, bool WIN>
 __global__ void __launch_bounds__(CMB_WARPS * 32) decode_combine_kernel(const DecArgs p, int G) {
   __shared__ int pre[260];
+  // WIN: waits first, as the attention kernel does (all rows of a padded batch may be empty); otherwise the
+  // plan, which comes from pos alone, is formed beside the attention's end.
+  if (WIN) ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  // from pos: no dependency on the previous kernel
   if (WIN) decode_window_prefix(p.win, p.pos, p.B, pre);
   else decode_tile_prefix(p.pos, p.B, p.L_max, pre);
   if (blockIdx.x == 0)
@@ -659,7 +664,7 @@ __global__ void __launch_bounds__(CMB_WARPS * 32) decode_combine_kernel(const De
   auto cta_of32 = [&](uint32_t x) { return ((x + 1) * uG - 1) / T; };
   auto owns = [&](uint32_t kk) { return (kk * T) / uG != ((kk + 1) * T) / uG; };
   const uint32_t k0 = cta_of32(ts), k1 = cta_of32(te - 1);
-  ptx::griddep_wait();  // the partials come from the attention kernel
+  if (!WIN) ptx::griddep_wait();  // the partials come from the attention kernel
   float M = -INFINITY, num[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.0f;
   uint32_t kk = k0;
   while (kk <= k1) {

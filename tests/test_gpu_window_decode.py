@@ -184,3 +184,44 @@ def test_caches_past_32_bit_offsets():
     out = T.window_decode_attn(Q, K, V, pos, n_kv, window, sink, SCALE)
     within(out[3:], ref, tol)
     assert L.tp_get_device_status(check=False) == L.TP_OK
+
+
+def test_positions_written_by_the_kernel_before():
+    """A device kernel writes pos (another type's cast, an addition) directly before the call, eagerly and in a
+    replayed graph: the result of positions that were there long before, bit for bit."""
+    n_heads, n_kv, B, L_max, window, sink = 16, 2, 64, 2048, 300, 4
+    Q, K, V = rnd(1, B, n_heads, 128).cuda(), rnd(2, 1, n_kv, B, L_max, 128).cuda(), rnd(3, 1, n_kv, B, L_max, 128).cuda()
+    ws = torch.empty(L.tp_window_decode_workspace_size(B, n_heads, n_kv, 128, 1), dtype=torch.uint8, device="cuda")
+    start = torch.randint(0, 900, (B,), generator=torch.Generator().manual_seed(4))
+    start[7] = start[8] = -1
+    steps = [start + 37 * k * (start >= 0) for k in range(1, 25)]
+    want = []
+    for p in steps:
+        pos = p.to(torch.int32).cuda()
+        torch.cuda.synchronize()
+        want.append(T.window_decode_attn(Q, K, V, pos, n_kv, window, sink, out=torch.zeros_like(Q, dtype=torch.bfloat16)))
+    torch.cuda.synchronize()
+    add = (37 * (start >= 0)).to(torch.int32).cuda()
+    out = torch.zeros(B, n_heads, 128, dtype=torch.bfloat16, device="cuda")
+    pos = start.to(torch.int32).cuda()
+    got = []
+    for p in steps:
+        pos.add_(add)
+        got.append(T.window_decode_attn(Q, K, V, pos, n_kv, window, sink, ws=ws, out=out.clone()))
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+    long = torch.stack(steps).cuda()
+    got = [T.window_decode_attn(Q, K, V, long[k].to(torch.int32), n_kv, window, sink, ws=ws, out=out.clone())
+           for k in range(len(steps))]
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+    pos.copy_(start.to(torch.int32))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pos.add_(add)
+        T.window_decode_attn(Q, K, V, pos, n_kv, window, sink, ws=ws, out=out)
+    got = []
+    for _ in steps:
+        graph.replay()
+        got.append(out.clone())
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+    assert L.tp_get_device_status(check=False) == L.TP_OK
