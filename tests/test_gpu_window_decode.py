@@ -225,3 +225,29 @@ def test_positions_written_by_the_kernel_before():
         got.append(out.clone())
     assert all(torch.equal(g, w) for g, w in zip(got, want))
     assert L.tp_get_device_status(check=False) == L.TP_OK
+
+
+def test_a_batch_of_empty_rows_keeps_the_order_of_the_stream():
+    """Kernels behind a decode step without work read what the kernels before it write: norm + rotation, an empty
+    step, then the rotation in place on the result of the first, against the same calls with waits between."""
+    n_heads, n_kv, N, B = 16, 2, 6000, 5
+    X = rnd(1, 1, N, (n_heads + 2 * n_kv) * 128).cuda()
+    f = T.rope_frequencies(128)
+    Q, K, V = rnd(2, B, n_heads, 128).cuda(), rnd(3, 1, n_kv, B, 256, 128).cuda(), rnd(4, 1, n_kv, B, 256, 128).cuda()
+    pos = torch.full((B,), -1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(L.tp_window_decode_workspace_size(B, n_heads, n_kv, 128, 1), dtype=torch.uint8, device="cuda")
+    out, O_buf = torch.empty_like(X), torch.zeros(B, n_heads, 128, dtype=torch.bfloat16, device="cuda")
+
+    def chain(wait):
+        T.qk_norm_rope_forward(X, n_heads, n_kv, inv_freq=f, out=out)
+        wait()
+        T.window_decode_attn(Q, K, V, pos, n_kv, 100, 4, ws=ws, out=O_buf)
+        wait()
+        T.qk_norm_rope_forward(out, n_heads, n_kv, inv_freq=f, out=out)
+        return out.clone()
+    want = chain(torch.cuda.synchronize)
+    for _ in range(20):
+        out.zero_()
+        assert torch.equal(chain(lambda: None), want)
+    assert not O_buf.any()
+    assert L.tp_get_device_status(check=False) == L.TP_OK
