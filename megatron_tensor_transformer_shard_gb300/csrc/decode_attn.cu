@@ -251,8 +251,9 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // WIN: this is the first kernel of the call, and the one before it on the stream may write pos, so
   // every thread waits for it before anything is read; then CTAs without a tile, which return below,
-  // are behind that kernel too, and so is whoever waits for this grid.  Otherwise the projection runs
-  // before, and the plan is formed beside its end.
+  // are behind that kernel too, and so is whoever waits for this grid.  Otherwise the projection's last
+  // kernel lets this one start only once it has waited itself, so pos is complete, and the plan is formed
+  // beside its end.
   if (WIN) ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   if (WIN) {

@@ -344,8 +344,10 @@ __device__ __forceinline__ float sk_sum(const SkGemmJob& j, uint32_t G, uint32_t
 
 template <int NB>
 __global__ void __launch_bounds__(256) skinny_reduce_kernel(const SkGemmJob j, int G) {
-  ptx::griddep_launch_dependents();
+  // Waits first: the decode attention behind forms its plan from pos, and zeroes the W_o counters, without a
+  // wait of its own, so it may start only once the GEMM, and with it all that came before the call, is complete.
   ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
   if (j.epi == SK_EPI_QKV && blockIdx.x == 0) decode_check_positions(j.pos, j.B, j.L_max, j.err);
   const int64_t n = static_cast<int64_t>(j.R) * j.B;
   for (int64_t idx = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; idx < n;

@@ -206,3 +206,47 @@ def test_decode_attn_full_size():
     got = Kd.cpu()
     for b, p in enumerate(pos):
         assert_close(f"cache {b}", _f16_f64(got[:, :, b, p]), ref["K_shards"][:, :, b, p])
+
+
+def test_positions_written_by_the_kernel_before():
+    """Token after token, pos advanced by a device kernel directly before each step: the same y and the same
+    caches, bit for bit, as with waits between the calls, eagerly and in a replayed graph."""
+    nh, nkv, t, B, L_max, steps = 8, 2, 2, 8, 600, 12
+    inp = I.decode_attn_inputs(B, nh * HD, nh, nkv, HD, L_max, seed=6)
+    w = T.DecodeAttnWeights(inp["W_qkv"].cuda(), inp["b_qkv"].cuda(), inp["W_o"].cuda(), inp["b_o"].cuda(), nh, nkv, HD, t)
+    caches = [_shard_cache(inp[c], nh, nkv, t) for c in "KV"]
+    x = inp["x"].cuda()
+    start = torch.tensor([0, 100, 126, 127, 128, 255, 500, 300], dtype=torch.int32, device="cuda")
+    ws = w.workspace(B, L_max, x.device)
+    y = torch.empty(B, nh * HD, dtype=torch.bfloat16, device="cuda")
+
+    def run(step, wait):
+        K, V = (c.clone() for c in caches)
+        ys = []
+        pos = start.clone()
+        for _ in range(steps):
+            step(K, V, pos, wait)
+            ys.append(y.clone())
+        torch.cuda.synchronize()
+        return ys, K, V
+
+    def eager(K, V, pos, wait):
+        pos.add_(1)
+        wait()
+        T.decode_attn_forward(x, w, K, V, pos, ws=ws, out=y)
+        wait()
+    want = run(eager, torch.cuda.synchronize)
+    graphs = {}
+
+    def replayed(K, V, pos, wait):
+        if K.data_ptr() not in graphs:
+            graphs[K.data_ptr()] = g = torch.cuda.CUDAGraph()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(g):
+                eager(K, V, pos, lambda: None)
+        graphs[K.data_ptr()].replay()
+    for step in (eager, replayed):
+        got = run(step, lambda: None)
+        assert all(torch.equal(a, b) for a, b in zip(got[0], want[0]))
+        assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+    assert L.tp_get_device_status(check=False) == L.TP_OK
