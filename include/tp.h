@@ -618,8 +618,9 @@ tp_status tp_attn_opt_backward(const tp_bf16* dY, const tp_bf16* X, const uint16
 
 /* Decode: tp_decode_attn_forward with `opt` (cu_seqlens and pos of `opt` are not used: the
  * token of sequence b is at pos[b], -1 for an empty row of a padded batch, whose y is
- * unspecified).  The projected rows are rounded to bf16 before the norm and rotation.  The
- * caches hold rotated keys; slots as tp_qk_norm_rope_append.  ws:
+ * unspecified).  The projected rows are rounded to IEEE fp16 before the norm and rotation, as
+ * the forward's are (a value above 65504 becomes infinite).  The caches hold rotated keys;
+ * slots as tp_qk_norm_rope_append.  ws:
  * tp_decode_attn_opt_workspace_size() bytes, 256-byte aligned. */
 size_t tp_decode_attn_opt_workspace_size(int64_t B, int64_t d, int n_heads, int n_kv_heads, int head_dim, int t);
 tp_status tp_decode_attn_opt_forward(const tp_bf16* x, int64_t B, int64_t d, int n_heads, int n_kv_heads, int head_dim,

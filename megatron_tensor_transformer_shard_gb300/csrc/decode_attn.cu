@@ -1086,7 +1086,7 @@ tp_status run_window_decode(const uint16_t* Q, int64_t B, int n_heads, int n_kv,
 namespace {
 
 struct OptWs {
-  uint16_t *rows, *q, *O;  // projected rows [B][t][R] bf16; rotated queries fp16 and O bf16 [B][nh][HD]
+  uint16_t *rows, *q, *O;  // projected rows [B][t][R] fp16; rotated queries fp16 and O bf16 [B][nh][HD]
   float* sk_part;
   void* core;
   size_t core_bytes, bytes;
@@ -1107,18 +1107,19 @@ OptWs opt_ws_layout(void* ws, int64_t B, int64_t d, int n_heads, int t, const De
   return w;
 }
 
-// y[b][r] = sum_k W[..][r][k] x[b][k] + bias[r] for B rows (slabs: the row-parallel shards of K).
+// y[b][r] = sum_k W[..][r][k] x[b][k] + bias[r] for B rows (slabs: the row-parallel shards of K), rounded
+// once from the fp32 sum, to bf16 or, y_f16, to fp16.
 tp_status project(const uint16_t* x, int64_t B, int64_t K, int64_t R, int slabs, const uint16_t* W, const uint16_t* bias,
-                  uint16_t* y, float* part, cudaStream_t s) {
+                  uint16_t* y, int y_f16, float* part, cudaStream_t s) {
   if (B >= 2 && B <= 32 && K % slabs == 0 && skinny_ok(R, K / slabs, static_cast<int>(B)) &&
       skinny_ok(R, K, static_cast<int>(B))) {
     SkGemmJob j;
     j.W = W; j.slabs = slabs; j.R = R; j.ku_per_slab = static_cast<int>(K / slabs / 128);
     j.x = x; j.ldx = K; j.B = static_cast<int>(B); j.part = part;
-    j.epi = SK_EPI_BF16; j.bias = bias; j.y = y; j.ldy = R; j.err = device_error_word();
+    j.epi = y_f16 ? SK_EPI_F16 : SK_EPI_BF16; j.bias = bias; j.y = y; j.ldy = R; j.err = device_error_word();
     return run_skinny_gemm(j, s);
   }
-  return run_row_gemv(x, B, K, R, slabs, W, bias, y, s);
+  return run_row_gemv(x, B, K, R, slabs, W, bias, y, s, y_f16);
 }
 
 }  // namespace
@@ -1140,7 +1141,6 @@ tp_status run_decode_opt(const uint16_t* x, int64_t B, int64_t d, int n_heads, i
   if (window == 0) window = L_max;
   QkNormRope nr = norm_rope;
   nr.pos = pos;
-  nr.flags |= TP_QKNR_BF16_INPUT;
   // the checks of both operators (no rows: nothing runs), before anything is launched
   TP_RETURN_IF(run_qk_norm_rope_append(nullptr, 0, n_heads, n_kv, head_dim, t, nr, nullptr, nullptr, nullptr, L_max, window,
                                        n_sink, rolling, s, 1));
@@ -1156,12 +1156,14 @@ tp_status run_decode_opt(const uint16_t* x, int64_t B, int64_t d, int n_heads, i
   if (ws_bytes < w.bytes) return TP_ERR_WORKSPACE;
   TP_RETURN_IF(ready());
   const int64_t nq = static_cast<int64_t>(n_heads) * HD;
-  TP_RETURN_IF(project(x, B, d, sh.R_t * t, 1, Wqkv_p, bqkv_p, w.rows, w.sk_part, s));
+  // The rows before norm and rotation are fp16, as the caches and the prompt's block hold them: a token that is
+  // appended here has the 2^-11 of one from a prefill (bf16 rows cost its key and value 2^-8).
+  TP_RETURN_IF(project(x, B, d, sh.R_t * t, 1, Wqkv_p, bqkv_p, w.rows, 1, w.sk_part, s));
   TP_RETURN_IF(run_qk_norm_rope_append(w.rows, B, n_heads, n_kv, head_dim, t, nr, w.q, Kc, Vc, L_max, window, n_sink,
                                        rolling, s, 1));
   TP_RETURN_IF(run_window_decode(w.q, B, n_heads, n_kv, head_dim, t, window, n_sink, rolling, scale, Kc, Vc, L_max, pos,
                                  w.O, w.core, w.core_bytes, s));
-  return project(w.O, B, nq, d, t, Wo_p, bo, y, w.sk_part, s);
+  return project(w.O, B, nq, d, t, Wo_p, bo, y, 0, w.sk_part, s);
 }
 
 }  // namespace tp

@@ -168,11 +168,6 @@ __device__ __forceinline__ void store_f16x32(uint16_t* dst, const float (&v)[32]
   }
 }
 
-__device__ __forceinline__ uint16_t float_to_f16_bits(float f) {
-  __half h = __float2half_rn(f);
-  return *reinterpret_cast<uint16_t*>(&h);
-}
-
 __device__ __forceinline__ void store_bf16x32(uint16_t* dst, const float (&v)[32]) {
   uint4* d4 = reinterpret_cast<uint4*>(dst);
 #pragma unroll

@@ -121,7 +121,7 @@ template <int M>
 __global__ void __launch_bounds__(GEMV_THREADS)
     down_reduce_kernel(const uint16_t* __restrict__ a, int64_t lda, int64_t h, int64_t F, int t,
                        const uint16_t* __restrict__ Wd, const uint16_t* __restrict__ bias,
-                       uint16_t* __restrict__ y) {
+                       uint16_t* __restrict__ y, int y_f16) {
   __shared__ float red[GEMV_WARPS][MAX_T * M];
   __shared__ float tot[MAX_T * M];
   const int64_t Ft = F / t;
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(GEMV_THREADS)
       float s = 0.0f;
       for (int i = 0; i < t; ++i) s += tot[i * M + m];  // g: fixed shard order
       if (bias) s += bf16_bits_to_float(bias[col]);      // once, after the sum
-      y[m * h + col] = float_to_bf16_bits(s);
+      y[m * h + col] = y_f16 ? float_to_f16_bits(s) : float_to_bf16_bits(s);
     }
   }
 }
@@ -179,19 +179,19 @@ tp_status launch_decode(const uint16_t* x, int64_t h, int64_t F, int t, const ui
   if (g2 > h) g2 = h;
   swiglu_gate_up_kernel<M><<<static_cast<unsigned>(g1), GEMV_THREADS, 0, s>>>(x, h, F, Wgu, a);
   TP_LAUNCHED();
-  down_reduce_kernel<M><<<static_cast<unsigned>(g2), GEMV_THREADS, 0, s>>>(a, F, h, F, t, Wd, nullptr, y);
+  down_reduce_kernel<M><<<static_cast<unsigned>(g2), GEMV_THREADS, 0, s>>>(a, F, h, F, t, Wd, nullptr, y, 0);
   TP_LAUNCHED();
   return TP_OK;
 }
 
 template <int M>
 tp_status launch_row(const uint16_t* a, int64_t K, int64_t h, int t, const uint16_t* Wd, const uint16_t* bias,
-                     uint16_t* y, cudaStream_t s) {
+                     uint16_t* y, int y_f16, cudaStream_t s) {
   int per_sm = 0;
   TP_CUDA_CHECK(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, down_reduce_kernel<M>, GEMV_THREADS, 0));
   int64_t g = static_cast<int64_t>(device_sm_count()) * (per_sm > 0 ? per_sm : 1);
   if (g > h) g = h;
-  down_reduce_kernel<M><<<static_cast<unsigned>(g), GEMV_THREADS, 0, s>>>(a, K, h, K, t, Wd, bias, y);
+  down_reduce_kernel<M><<<static_cast<unsigned>(g), GEMV_THREADS, 0, s>>>(a, K, h, K, t, Wd, bias, y, y_f16);
   TP_LAUNCHED();
   return TP_OK;
 }
@@ -201,7 +201,7 @@ tp_status launch_row(const uint16_t* a, int64_t K, int64_t h, int t, const uint1
 // Row-parallel GEMV followed by g: y[m] = sum_{i<t} a[m][C_i] W_i^T + bias (once),
 // a [M][K], W [t][h][K/t].  Rows are taken 8 at a time (each group re-streams W).
 tp_status run_row_gemv(const uint16_t* a, int64_t M, int64_t K, int64_t h, int t, const uint16_t* Wd,
-                       const uint16_t* bias, uint16_t* y, cudaStream_t s) {
+                       const uint16_t* bias, uint16_t* y, cudaStream_t s, int y_f16) {
   if (M < 0 || K < 1 || h < 1 || t < 1) return TP_ERR_INVALID_ARG;
   if (t > MAX_T || K % t != 0 || (K / t) % 8 != 0) return TP_ERR_SHAPE;
   if (M == 0) return TP_OK;
@@ -211,14 +211,14 @@ tp_status run_row_gemv(const uint16_t* a, int64_t M, int64_t K, int64_t h, int t
     uint16_t* ym = y + m0 * h;
     tp_status st;
     switch (mg) {
-      case 1: st = launch_row<1>(am, K, h, t, Wd, bias, ym, s); break;
-      case 2: st = launch_row<2>(am, K, h, t, Wd, bias, ym, s); break;
-      case 3: st = launch_row<3>(am, K, h, t, Wd, bias, ym, s); break;
-      case 4: st = launch_row<4>(am, K, h, t, Wd, bias, ym, s); break;
-      case 5: st = launch_row<5>(am, K, h, t, Wd, bias, ym, s); break;
-      case 6: st = launch_row<6>(am, K, h, t, Wd, bias, ym, s); break;
-      case 7: st = launch_row<7>(am, K, h, t, Wd, bias, ym, s); break;
-      default: st = launch_row<8>(am, K, h, t, Wd, bias, ym, s); break;
+      case 1: st = launch_row<1>(am, K, h, t, Wd, bias, ym, y_f16, s); break;
+      case 2: st = launch_row<2>(am, K, h, t, Wd, bias, ym, y_f16, s); break;
+      case 3: st = launch_row<3>(am, K, h, t, Wd, bias, ym, y_f16, s); break;
+      case 4: st = launch_row<4>(am, K, h, t, Wd, bias, ym, y_f16, s); break;
+      case 5: st = launch_row<5>(am, K, h, t, Wd, bias, ym, y_f16, s); break;
+      case 6: st = launch_row<6>(am, K, h, t, Wd, bias, ym, y_f16, s); break;
+      case 7: st = launch_row<7>(am, K, h, t, Wd, bias, ym, y_f16, s); break;
+      default: st = launch_row<8>(am, K, h, t, Wd, bias, ym, y_f16, s); break;
     }
     TP_RETURN_IF(st);
   }

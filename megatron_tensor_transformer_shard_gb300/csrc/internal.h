@@ -198,7 +198,7 @@ tp_status pack_qkv_gqa_bias(const uint16_t* b, int n_heads, int n_kv, int head_d
                             cudaStream_t s);
 
 // skinny GEMM (skinny_gemm.cu): y[b][r] = sum_k W[r][k] x[b][k] for 1..32 rows of x.
-enum SkEpilogue : int { SK_EPI_BF16 = 0, SK_EPI_QKV = 1 };
+enum SkEpilogue : int { SK_EPI_BF16 = 0, SK_EPI_QKV = 1, SK_EPI_F16 = 2 };
 struct SkGemmJob {
   const uint16_t* W = nullptr;  // [slabs][R][Kt] bf16, Kt = 128 * ku_per_slab
   int slabs = 1;
@@ -211,7 +211,7 @@ struct SkGemmJob {
   int nrb = 0, nku = 0;         // set by run_skinny_gemm
   int epi = SK_EPI_BF16;
   const uint16_t* bias = nullptr;  // [R] nullable, added once after the full K sum
-  uint16_t* y = nullptr;           // SK_EPI_BF16: y[b * ldy + r]
+  uint16_t* y = nullptr;           // SK_EPI_BF16, SK_EPI_F16: y[b * ldy + r]
   int64_t ldy = 0;
   // SK_EPI_QKV: packed decode QKV rows [t][R_t], routed to q (fp16) or the cache copies
   int64_t R_t = 0, L_max = 0;
@@ -274,8 +274,9 @@ tp_status run_decode_opt(const uint16_t* x, int64_t B, int64_t d, int n_heads, i
                          int64_t window, int64_t n_sink, int rolling, const QkNormRope& norm_rope, const uint16_t* Wqkv_p,
                          const uint16_t* bqkv_p, const uint16_t* Wo_p, const uint16_t* bo, uint16_t* Kc, uint16_t* Vc,
                          int64_t L_max, const int32_t* pos, uint16_t* y, void* ws, size_t ws_bytes, cudaStream_t s);
+// y in bf16, or IEEE fp16 with y_f16.
 tp_status run_row_gemv(const uint16_t* a, int64_t M, int64_t K, int64_t h, int t, const uint16_t* Wd,
-                       const uint16_t* bias, uint16_t* y, cudaStream_t s);
+                       const uint16_t* bias, uint16_t* y, cudaStream_t s, int y_f16 = 0);
 
 // decode GEMV (gemv.cu), LayerNorm (layernorm.cu)
 tp_status run_decode_swiglu(const uint16_t* x, int64_t M, int64_t h, int64_t F, int t, const uint16_t* Wgu,

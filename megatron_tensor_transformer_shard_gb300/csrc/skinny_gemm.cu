@@ -356,8 +356,8 @@ __global__ void __launch_bounds__(256) skinny_reduce_kernel(const SkGemmJob j, i
     const int64_t r = idx - static_cast<int64_t>(b) * j.R;
     float v = sk_sum<NB>(j, static_cast<uint32_t>(G), static_cast<uint32_t>(r), b);
     if (j.bias) v += bf16_bits_to_float(j.bias[r]);
-    if (j.epi == SK_EPI_BF16) {
-      j.y[static_cast<int64_t>(b) * j.ldy + r] = float_to_bf16_bits(v);
+    if (j.epi != SK_EPI_QKV) {
+      j.y[static_cast<int64_t>(b) * j.ldy + r] = j.epi == SK_EPI_F16 ? float_to_f16_bits(v) : float_to_bf16_bits(v);
     } else {  // SK_EPI_QKV: route the coordinate to Q or to the shard's cache copy (fp16)
       const __half hv = __float2half_rn(v);
       const uint16_t bits = *reinterpret_cast<const uint16_t*>(&hv);

@@ -166,3 +166,45 @@ def test_decode_without_options_is_the_plain_decode():
     y = T.decode_attn_forward(dev["x"], w, K.clone(), V.clone(), pos)
     y2 = T.decode_attn_forward(dev["x"], w, K, V, pos, attn=T.AttentionOptions())
     assert_close("y", f64(y2), f64(y))
+
+
+@pytest.mark.parametrize("B,n_heads,n_kv,t,L_max", [(1, 8, 2, 2, 16384), (8, 8, 2, 2, 4096), (40, 4, 4, 1, 300)])
+def test_decode_without_options_gives_the_bits_of_the_plain_decode(B, n_heads, n_kv, t, L_max):
+    """The same projection, rounded once to fp16, and as many tiles as CTAs or more on both sides, so the same cut."""
+    inp = I.decode_attn_inputs(B, n_heads * 128, n_heads, n_kv, 128, L_max, seed=1)
+    dev = {k: v.cuda() for k, v in inp.items()}
+    w = T.DecodeAttnWeights(dev["W_qkv"], dev["b_qkv"], dev["W_o"], dev["b_o"], n_heads, n_kv, 128, t)
+    K, V = (dev[c].view(w.cache_shape(B, L_max)) for c in "KV")
+    pos = torch.randint(0, L_max, (B,), generator=torch.Generator().manual_seed(2)).to(torch.int32).cuda()
+    pos[0] = L_max - 1
+    K1, V1, K2, V2 = K.clone(), V.clone(), K.clone(), V.clone()
+    y = T.decode_attn_forward(dev["x"], w, K1, V1, pos)
+    y2 = T.decode_attn_forward(dev["x"], w, K2, V2, pos, attn=T.AttentionOptions())
+    assert torch.equal(K2, K1) and torch.equal(V2, V1) and torch.equal(y2, y)
+    assert not torch.equal(K1, K)
+
+
+@pytest.mark.parametrize("B", [1, 5, 40])
+def test_decode_holds_its_rows_in_fp16(B):
+    """The cached value is the projection rounded once to fp16, with norms and rotation on: half a step, and an
+    fp32 sum of 512 products (512 half steps of fp32 on the sum of absolute values at most)."""
+    n_heads, n_kv, t = 4, 2, 2
+    inp = I.decode_attn_inputs(B, 512, n_heads, n_kv, 128, 4, seed=3)
+    dev = {k: v.cuda() for k, v in inp.items()}
+    w = T.DecodeAttnWeights(dev["W_qkv"], dev["b_qkv"], dev["W_o"], dev["b_o"], n_heads, n_kv, 128, t)
+    opt, host = options(True, 128, 4, 1)
+    K, V = (torch.zeros(w.cache_shape(B, 4), dtype=torch.float16, device="cuda") for _ in range(2))
+    T.decode_attn_forward(dev["x"], w, K, V, torch.zeros(B, dtype=torch.int32, device="cuda"), attn=opt)
+    x, Wq, bq = f64(inp["x"]), f64(w.Wqkv_p), f64(w.bqkv_p)
+    for i in range(t):
+        rows, mag = x @ Wq[i].T + bq[i], np.abs(x) @ np.abs(Wq[i]).T + np.abs(bq[i])
+        got, ref = f64(V[i, 0, :, 0]), rows[:, -128:]
+        assert (np.abs(got - ref) <= 2.0 ** -11 * np.abs(ref) + 512 * 2.0 ** -24 * mag[:, -128:] + 2.0 ** -25).all()
+        # position 0 is not rotated: the normed key, whose roundings the oracle's tolerance counts, of a row off by
+        # as much as the value (twice: the norm's factor)
+        key, tol = O.qk_norm_rope(rows[None], n_heads // t, 1, host["gq"], host["gk"], 1e-5)
+        part, gain = slice(256, 384), np.abs(host["gk"]) / np.sqrt((rows[:, 256:384] ** 2).mean(1, keepdims=True))
+        off = 2.0 ** -11 * np.abs(rows[:, part]) + 512 * 2.0 ** -24 * mag[:, part] + 2.0 ** -25
+        off = (off + np.abs(rows[:, part]) * (off ** 2).mean(1, keepdims=True) ** 0.5 /
+               np.sqrt((rows[:, part] ** 2).mean(1, keepdims=True))) * gain
+        assert (np.abs(f64(K[i, 0, :, 0]) - key[0][:, part]) <= tol[0][:, part] + off).all()
