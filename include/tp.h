@@ -536,10 +536,12 @@ tp_status tp_attn_core_backward(const uint16_t* QKV, const tp_bf16* O, const uin
  * Backward: dO [t][N][d/t] IEEE fp16; O and lse from the forward; Dvec [t][n_heads/t][N] fp32
  * scratch; dQKV [t][N][R], bf16, or fp16 with flags = TP_ATTN_F16_INPUT: every element is
  * written, 0 in rows of no sequence.  Q, K, V, dO, O and lse of the sequences' rows are
- * finite (a non-finite one spreads to rows of its 128-row block).  Deterministic.  ws:
+ * finite (a non-finite one spreads to rows of its 128-row block).  dO may be of any magnitude, down
+ * to where fp16 itself loses bits (below 2^-14): P (dP - D) is held in fp16 under powers of two
+ * taken from the largest |dO| (of 32 rows for dQ, of a KV head for dK) and sum |v|.  Deterministic.  ws:
  * tp_attn_window_backward_workspace_size() bytes, 256-byte aligned (fp32 partial dK, dV of
  * the sinks: 2 KB for each KV head of a shard, sink and chunk of about max(window, 128) rows,
- * 2048 at most; the row spans of cu_seqlens).  Two to four launches.  N == 0 is a no-op. */
+ * 2048 at most; the row spans of cu_seqlens).  Three or four launches.  N == 0 is a no-op. */
 size_t tp_attn_window_forward_workspace_size(int64_t N, int64_t n_seq);
 tp_status tp_attn_window_forward(const uint16_t* QKV, int64_t N, int64_t d, int n_heads, int n_kv_heads, int head_dim,
                                  int t, int64_t window, int64_t n_sink, float scale, const int32_t* cu_seqlens,

@@ -40,9 +40,19 @@
 // causal 2535 us (1735); dQ 698 us, dK / dV 830 us at W 1024 (SM throughput 77 and 88 %, the longest CTA
 // of dK / dV 96 %).
 //
-// P and dS are rounded to fp16 (2^-11, relative; 2^-25 absolute against a row sum of at least 1)
-// because the MMA takes 16-bit operands; scores, row maxima and sums, lse, D and every
-// accumulator stay fp32.
+// P and dS are rounded to fp16 (2^-11, relative) because the MMA takes 16-bit operands; scores, row
+// maxima and sums, lse, D and every accumulator stay fp32.  Near zero fp16 has 2^-25 absolute.  Against
+// the forward's row sum of at least 1 that is nothing; but a row of P under a wide window, and dS with
+// dO's magnitude in it, may lie there altogether.  So the backward holds P 2^13 and dS 2^e, and takes the
+// powers of two out with the fp32 results: they shift exponents, and change no other bit.  |dO . v| is
+// at most B = max|dO| max sum|v|, |D| as much (and 2^-8 for O's rounding), so e = 13 - floor(log2 B)
+// keeps |dS| 2^e below 33,000, all bits of what is above 2^-27 B, and steps of 2^-37 B below, whatever the
+// magnitudes of dO and V.  dQ has an e for every 32 query rows, with the v's of the key blocks that their tile
+// sees; dK sums over queries, so it has one for each KV head, from the largest B of all rows.
+// Before dQ, window_prep_kernel takes the largest sum|v| of each key block; it, and then the largest
+// B of a KV head, wait in places of the outputs that are free at the time: value_bound(), row_bound().
+// Measured, backward at N 16384, 64 / 8 heads, W 1024, seven sequences, and at N 2048, 96 / 96 heads, W 512:
+// 1384 and 222 us with dS as it was, 1407 and 233 so.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -820,6 +830,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
 // the TMEM lanes, looping over 64-query blocks of the group's heads; dQ per 128-query block over
 // 64-key blocks.  The scores of a block are formed again from the saved lse.  A hidden pair's P and
 // dS are selected to 0, whatever its operands hold.
+constexpr int P_EXP = 13;              // P 2^13: at most 1 but for lse's error, which has 2^2 of room
 constexpr int BWD_THREADS = 320;       // TMA warp, MMA warp, eight compute warps
 constexpr int BWD_STAGES = 4;
 constexpr int DKV_SMEM = 1024 + 2 * TILE + BWD_STAGES * (2 * TILE64 + 512) + 256 + QUEUE_SMEM;
@@ -828,7 +839,26 @@ constexpr int DQ_STAGES = 4;
 // The next block of queries is asked for this many steps before the last loads, as its D has to be there when
 // the block before ends: 0 and 3 steps took 651 and 636 us (N 16384, W 1024, seven sequences), 6 take 632.
 constexpr int DQ_AHEAD = 6;
-constexpr int DQ_SMEM = 1024 + 2 * TILE + DQ_STAGES * 2 * TILE64 + 256 + QUEUE_SMEM + 2 * 128 * 4;
+constexpr int DQ_SMEM = 1024 + 2 * TILE + DQ_STAGES * 2 * TILE64 + 256 + QUEUE_SMEM + 2 * (128 + 4) * 4;
+// With 1 KB of the system's the block stays within the 196 KB split of an SM's memory, so 60 KB of it cache the output
+// warps' loads; one KB more takes the 228 KB split, 672 us where this takes 645 (N 16384, W 1024, seven sequences).
+static_assert(DQ_SMEM + 1024 <= 196 * 1024, "the next larger shared memory split");
+
+// The largest sum|v| of a key block: in dV, 64 blocks a row, until the dK / dV kernel, behind dQ's, writes that.
+__device__ __forceinline__ float* value_bound(const WinArgs& p, int shard, int vcol, int kb) {
+  return reinterpret_cast<float*>(p.dQKV + (static_cast<int64_t>(shard) * p.N + kb / 64) * p.row_w + vcol) + kb % 64;
+}
+// The largest B of the query heads that share head jj's KV head, as the bits of a float that is not negative: in the
+// place of D of the first such head's row 0, a row that sees one key, whose D has no use.
+__device__ __forceinline__ unsigned* row_bound(const WinArgs& p, int shard, int jj) {
+  return reinterpret_cast<unsigned*>(p.Dvec + (static_cast<int64_t>(shard) * p.hpr + jj / p.Gs * p.Gs) * p.N);
+}
+// e of a bound B, and 2^e.
+__device__ __forceinline__ int ds_exponent(float bound) {
+  const int x = static_cast<int>(__float_as_uint(bound) >> 23) - 127;  // floor(log2 B), -127 for 0
+  return max(-30, min(P_EXP - x, 64));  // finite fp16 operands: B is 0 or 2^-48 .. 2^39
+}
+__device__ __forceinline__ float power2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 // The first 64-query block beyond the window's reach of key block kb: the block's own CTA takes the
 // queries before it, the far CTAs those from it on (only sinks are seen from there).
@@ -838,14 +868,14 @@ __device__ __forceinline__ int reach64(const WinArgs& p, int kb) { return (kb * 
 // (2.4e-3 of the whole gradient under a window of 1).  Its dS is 0.
 __device__ __forceinline__ bool sees_one(const WinArgs& p, int q, int st) { return q == st || (p.W == 1 && p.S == 0); }
 
-// P and dS of one key row (or query row) and 32 scores: p = 2^(s sl2 + nl), d = p (dp + nd), packed
-// fp16.  ROWQ: nl, nd are the row's (dQ); else nlv, ndv hold one per column (dK / dV, shared memory).  Unless
-// plain, p is 0 outside bits and d outside dbits.
+// P and dS of one key row (or query row) and 32 scores: p = 2^(s sl2 + nl), d = p (dp up + nd), packed
+// fp16; up and the powers of two in nd (and nl) make them d 2^e (and p 2^13).  ROWQ: nl, nd are the row's (dQ);
+// else nlv, ndv hold one per column (dK / dV, shared memory).  Unless plain, p is 0 outside bits and d outside dbits.
 template <bool ROWQ>
 __device__ __forceinline__ void p_ds32(const uint32_t (&s)[32], const uint32_t (&dp)[32], float sl2, float nl, float nd,
-                                       const float4* nlv, const float4* ndv, bool plain, uint32_t bits,
+                                       float up, const float4* nlv, const float4* ndv, bool plain, uint32_t bits,
                                        uint32_t dbits, uint32_t (&wp)[16], uint32_t (&wds)[16]) {
-  const uint64_t sl2x2 = f2_pack(sl2, sl2), nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+  const uint64_t sl2x2 = f2_pack(sl2, sl2), nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd), up2 = f2_pack(up, up);
 #pragma unroll
   for (int e4 = 0; e4 < 8; ++e4) {
     float4 L4, D4;
@@ -862,7 +892,8 @@ __device__ __forceinline__ void p_ds32(const uint32_t (&s)[32], const uint32_t (
       f2_unpack(f2_fma(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sl2x2, a), x0, x1);
       float p0 = ptx::exp2_approx(x0), p1 = ptx::exp2_approx(x1);
       float d0, d1;
-      f2_unpack(f2_mul(f2_pack(p0, p1), f2_add(f2_pack(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), d)), d0, d1);
+      f2_unpack(f2_mul(f2_pack(p0, p1), f2_fma(f2_pack(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), up2, d)), d0,
+                d1);
       if (!plain) {
         if (!ROWQ) {
           p0 = (bits >> e) & 1u ? p0 : 0.0f;
@@ -887,8 +918,9 @@ __device__ __forceinline__ Sight sight_of(uint32_t bits) {
 // One thread's 32 scores and dP of a step in TMEM to P and dS, written over their first 16 columns (P only
 // where it is an operand: dK / dV).  Columns that no row of the warp sees become 0 without the arithmetic.
 template <bool ROWQ>
-__device__ __forceinline__ void p_ds_step(uint32_t tS, uint32_t tdP, float sl2, float nl, float nd, const float4* nlv,
-                                          const float4* ndv, uint32_t bits, uint32_t dbits, Sight sight) {
+__device__ __forceinline__ void p_ds_step(uint32_t tS, uint32_t tdP, float sl2, float nl, float nd, float up,
+                                          const float4* nlv, const float4* ndv, uint32_t bits, uint32_t dbits,
+                                          Sight sight) {
   uint32_t wp[16], wds[16];
   if (sight == SEES_NONE) {
 #pragma unroll
@@ -898,8 +930,8 @@ __device__ __forceinline__ void p_ds_step(uint32_t tS, uint32_t tdP, float sl2, 
     ptx::tmem_ld32(tS, s);
     ptx::tmem_ld32(tdP, dp);
     ptx::tmem_ld_wait();
-    if (sight == SEES_ALL) p_ds32<ROWQ>(s, dp, sl2, nl, nd, nlv, ndv, true, 0u, 0u, wp, wds);
-    else p_ds32<ROWQ>(s, dp, sl2, nl, nd, nlv, ndv, false, bits, dbits, wp, wds);
+    if (sight == SEES_ALL) p_ds32<ROWQ>(s, dp, sl2, nl, nd, up, nlv, ndv, true, 0u, 0u, wp, wds);
+    else p_ds32<ROWQ>(s, dp, sl2, nl, nd, up, nlv, ndv, false, bits, dbits, wp, wds);
   }
   if (ROWQ) {
     ptx::tmem_st16(tS, wds);
@@ -938,6 +970,7 @@ __device__ __forceinline__ void zero_row128(uint8_t* row) {
 struct DkvWork {
   int far, kvh, shard, jl, kb, q_first, q_end, chunk, far_st, kcol, vcol;
   int st, en;  // the sequence of the block's rows, -1: not one for all rows
+  int e;       // dS 2^e
   DkvWork() = default;
   __device__ DkvWork(const WinArgs& p, int w, int total) {
     far = w < p.nfar;
@@ -969,6 +1002,7 @@ struct DkvWork {
     q_end = max(q_end, q_first);
     st = common_begin(p, kb * BKV, BKV, total);
     en = span_of(p, kb * BKV).y;
+    e = ds_exponent(__uint_as_float(*row_bound(p, shard, jl * p.Gs)));
   }
   __device__ int nq() const { return q_end - q_first; }
 };
@@ -1079,10 +1113,11 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         for (int e = 0; e < 2; ++e) {
           const int q = qi * 64 + lane + 32 * e;
           nl[e] = q < p.N ? p.lse[vec + q] : 0.0f;
-          nd[e] = q < p.N ? p.Dvec[vec + q] : 0.0f;
+          nd[e] = q < p.N && q > 0 ? p.Dvec[vec + q] : 0.0f;  // row 0: row_bound()
         }
       };
       load_row();
+      const float up = power2(k.e - P_EXP);
       for (int n = 0; n < nloop; ++n, ++issued) {
         const uint32_t slot = issued % BWD_STAGES;
         const int q0 = qi * 64, qcol = qh * HD;
@@ -1105,10 +1140,10 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
           tma_tile64(dst + TILE64, &tm_do, &qd_full[slot], qcol, q0, k.shard);
         }
         float* ld = sLD + slot * 128 + lane;
-        ld[0] = -(l0 * kLog2e);
-        ld[32] = -(l1 * kLog2e);
-        ld[64] = -d0;
-        ld[96] = -d1;
+        ld[0] = P_EXP - l0 * kLog2e;
+        ld[32] = P_EXP - l1 * kLog2e;
+        ld[64] = -d0 * up;
+        ld[96] = -d1 * up;
         ptx::mbar_arrive(&qd_full[slot]);
       }
       if (ok) advance();
@@ -1212,6 +1247,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
       const bool sink = alive && kv < sp.x + p.S;
       const bool alone = alive && sees_one(p, kv, sp.x);
       const int qmax = !alive ? -1 : sink ? sp.y - 1 : min(kv + p.W - 1, sp.y - 1);
+      const float up = power2(k.e - P_EXP);
       int qi = k.q_first - 1;  // (group head, query block) pairs, without a division on the way to the scores
       for (int i = 0; i < nloop; ++i, ++n) {
         const uint32_t b = n & 1, slot = n % BWD_STAGES;
@@ -1230,7 +1266,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         const float4* dd = reinterpret_cast<const float4*>(sLD + slot * 128 + 64 + 32 * h);
         // the query of this key's own row, when it sees nothing else
         const uint32_t own = alone && kv >= c0 && kv < c0 + 32 ? 1u << (kv - c0) : 0u;
-        p_ds_step<false>(tSb, tdPb, p.scale_log2, 0.f, 0.f, l2, dd, bits, bits & ~own, sight);
+        p_ds_step<false>(tSb, tdPb, p.scale_log2, 0.f, 0.f, up, l2, dd, bits, bits & ~own, sight);
         if (total < p.N && qi * 64 + 64 > total) {
           // Q and dO rows behind the last sequence may hold anything: zero them before the dV, dK MMAs
           // multiply them with P = dS = 0 (four panels of 64 rows, 256 threads)
@@ -1269,15 +1305,17 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 64; ++e) r[e >> 5][e & 31] = 0u;
         }
+        const float down = power2(part ? -k.e : -P_EXP);
         if (partial && ok) {
           float* dst = frow + part * HD + 64 * h;
 #pragma unroll
           for (int e = 0; e < 64; e += 4) {
             const uint32_t* v = &r[e >> 5][e & 31];
-            *reinterpret_cast<uint4*>(dst + e) = make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(dst + e) = make_float4(__uint_as_float(v[0]) * down, __uint_as_float(v[1]) * down,
+                                                              __uint_as_float(v[2]) * down, __uint_as_float(v[3]) * down);
           }
         } else if (!k.far && ok && kv < p.N) {
-          const float mul = part ? p.scale : 1.0f;
+          const float mul = part ? p.scale * down : down;
           uint16_t* dst = drow + (part ? k.kcol : k.vcol) + 64 * h;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -1303,6 +1341,12 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
   }
+}
+
+// The larger magnitudes of two pairs of fp16.
+__device__ __forceinline__ __half2 max_abs2(__half2 m, uint32_t x) {
+  x &= 0x7fff7fffu;
+  return __hmax2(m, *reinterpret_cast<const __half2*>(&x));
 }
 
 // One 128-query block of a head and the 64-key blocks that it sees.
@@ -1348,7 +1392,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 13 + 2 * DQ_STAGES);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   WorkQueue<DqWork, 13> queue(reinterpret_cast<uint8_t*>(bars) + 256);
-  volatile float* sD =  // [2][128]
+  volatile float* sD =  // of two blocks in turn, 2^e D [128] of the rows, then 2^e [4] of each 32
       reinterpret_cast<volatile float*>(reinterpret_cast<uint8_t*>(bars) + 256 + QUEUE_SMEM);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1504,11 +1548,12 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
       const int64_t vec = (static_cast<int64_t>(k.shard) * p.hpr + k.jj) * p.N;
       const bool alive = q < total;
       const float nl = alive ? -(p.lse[vec + q] * kLog2e) : 0.0f;
-      float nd = 0.0f;
+      float nd = 0.0f, up = 1.0f;
       if (nkv > 0) {
         ok = warp_wait(&d_full[blocks & 1], (blocks >> 1) & 1, abort_flag, p.err, ERR_WIN_SOFTMAX, p.timeout_ns);
         if (!ok) break;
-        nd = -sD[(blocks & 1) * 128 + quad * 32 + lane];
+        nd = -sD[(blocks & 1) * 132 + quad * 32 + lane];
+        up = sD[(blocks & 1) * 132 + 128 + quad];
       }
       const int st = !alive ? 0 : k.st >= 0 ? k.st : span_of(p, q).x;
       const bool sees = alive && !sees_one(p, q, st);
@@ -1525,7 +1570,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         }
         ptx::tc_fence_after();
         const uint32_t tSb = tmem + 64 * b + lane_base + 32 * h, tdPb = tSb + 128;
-        p_ds_step<true>(tSb, tdPb, p.scale_log2, nl, nd, nullptr, nullptr, bits, bits, sight);
+        p_ds_step<true>(tSb, tdPb, p.scale_log2, nl, nd, up, nullptr, nullptr, bits, bits, sight);
         if (total < p.N && k0 + 64 > total) {
           // K rows behind the last sequence may hold anything: zero them before the dQ MMA multiplies
           // them with dS = 0 (two panels of 64 rows)
@@ -1543,12 +1588,20 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
       if (nkv > 0) ++blocks;
     }
   } else {
-    // Output warps: D of a block before the compute warps come to it, dQ of the one before while they are at
-    // it; a row a thread.  (D = rowsum(dO O) as a kernel of its own took 83 us at N 16384, 64 heads; by the compute
+    // Output warps: D, and the e of dS, of a block before the compute warps come to it, dQ of the one before while
+    // they are at it; a row a thread.  (D = rowsum(dO O) as a kernel of its own took 83 us at N 16384, 64 heads; by the compute
     // warps from an O tile beside Q and dO it was 2,400 of 27,000 cycles of a block: 656 us for the kernel, not 632.)
     const int quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
-    auto form_d = [&](const DqWork& k, uint32_t block) {
+    auto form_d = [&](const DqWork& k, uint32_t block) {  // returns 2^-e of this warp's rows
+      // the largest sum|v| of the key blocks that the tile sees, the first 32 of them beside dO and O
+      const int a0 = k.l.a0 >> 1, na = k.l.a1 > k.l.a0 ? ((k.l.a1 + 1) >> 1) - a0 : 0, b0 = k.l.b0 >> 1;
+      const int nv = na + ((k.l.b1 + 1) >> 1) - b0;
+      auto v_at = [&](int i) {
+        return i < nv ? *value_bound(p, k.shard, k.vcol, i < na ? a0 + i : b0 + i - na) : 0.0f;
+      };
+      float vm = v_at(lane);
+      __half2 top = __float2half2_rn(0.0f);  // max|dO| of the rows
       // half a warp a row, 16 rows in flight
       const int half = lane >> 4;
       const int64_t at =
@@ -1574,6 +1627,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             unpack_bf16x2(ow[e], o0, o1);
             unpack_f16x2(gw[e], g0, g1);
             sum = fmaf(g0, o0, fmaf(g1, o1, sum));
+            top = max_abs2(top, gw[e]);
           }
 #pragma unroll
           for (int m = 8; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
@@ -1581,10 +1635,23 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
           if (lane < rows && (lane & ~1) == r0 + 2 * u) D = lane & 1 ? odd : even;
         }
       }
-      sD[(block & 1) * 128 + row] = D;  // 0 for the rows behind the last sequence
-      if (lane < rows) p.Dvec[(static_cast<int64_t>(k.shard) * p.hpr + k.jj) * p.N + k.qb * BQ + row] = D;  // for dK, dV
+#pragma unroll 4
+      for (int i = lane + 32; i < nv; i += 32) vm = fmaxf(vm, v_at(i));
+      auto warp_max = [](float x) {  // of values that are not negative
+        return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+      };
+      const float bound = warp_max(__half2float(__hmax(__low2half(top), __high2half(top)))) * warp_max(vm);
+      const int e = ds_exponent(bound);
+      const float up = power2(e);
+      sD[(block & 1) * 132 + row] = D * up;  // 0 for the rows behind the last sequence
+      if (lane == 0) sD[(block & 1) * 132 + 128 + quad] = up;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&d_full[block & 1]);
+      // for dK, dV
+      const int64_t vec = (static_cast<int64_t>(k.shard) * p.hpr + k.jj) * p.N;
+      if (lane < rows && k.qb * BQ + row > 0) p.Dvec[vec + k.qb * BQ + row] = D;
+      if (lane == 0) atomicMax(row_bound(p, k.shard, k.jj), __float_as_uint(bound));  // a maximum: the order does not matter
+      return power2(-e);
     };
     auto row_of = [&](const DqWork& k) {
       return p.dQKV + (static_cast<int64_t>(k.shard) * p.N + k.qb * BQ + row) * p.row_w + k.jj * HD;
@@ -1592,11 +1659,12 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     uint32_t blocks = 0;  // whose D is formed
     DqWork k;
     uint16_t* out = nullptr;  // this thread's row of the block whose dQ is to be stored
+    float mul = 0.0f, mul_new = 0.0f;  // .. and its factor, scale 2^-e, and that of the block being formed
     bool stores = false, more = true;
     while (more) {
       more = queue.read<true>(k, abort_flag, p.err, ERR_WIN_SOFTMAX, p.timeout_ns);
       const bool work = more && k.count() > 0;
-      if (work) form_d(k, blocks);
+      if (work) mul_new = p.scale * form_d(k, blocks);
       if (stores && (work || !more)) {
         const uint32_t done = blocks - 1, pb = done & 1;
         if (!warp_wait(&acc_full[pb], (done >> 1) & 1, abort_flag, p.err, ERR_WIN_SOFTMAX, p.timeout_ns)) break;
@@ -1617,8 +1685,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
               uint32_t v[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const float x0 = __uint_as_float(r[16 * u + 2 * e]) * p.scale;
-                const float x1 = __uint_as_float(r[16 * u + 2 * e + 1]) * p.scale;
+                const float x0 = __uint_as_float(r[16 * u + 2 * e]) * mul;
+                const float x1 = __uint_as_float(r[16 * u + 2 * e + 1]) * mul;
                 v[e] = p.dqkv_f16 ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
               }
               store_16(out + 32 * c + 16 * u, v, p.wide);
@@ -1629,6 +1697,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
       if (!more) break;
       if (work) {
         out = k.qb * BQ + row < p.N ? row_of(k) : nullptr;
+        mul = mul_new;
         stores = true;
         ++blocks;
       } else if (k.qb * BQ + row < p.N) {  // a block behind the last sequence
@@ -1707,18 +1776,15 @@ __global__ void __launch_bounds__(SINK_THREADS) window_sink_kernel(const WinArgs
 // --------------------------------------------------------------- sequences
 // span[r] = the (begin, end) of row r's sequence, from the n + 1 boundaries in cu; end = r: none
 // (behind the last).  Boundaries that are out of order or out of range are reported, and clamped
-// so that every span holds its row and stays in [0, N).
-__global__ void __launch_bounds__(256) window_spans_kernel(const int32_t* cu, int n, int N, int* total_out, int2* span,
-                                                           int* err) {
-  ptx::griddep_wait();
-  ptx::griddep_launch_dependents();
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+// so that every span holds its row and stays in [0, N).  Called by `threads` >= N threads, i = 0, 1, ..
+__device__ __forceinline__ void write_spans(const int32_t* cu, int n, int N, int* total_out, int2* span, int* err,
+                                            int64_t i, int64_t threads) {
   const int total = max(0, min(cu[n], N));
   if (i == 0) {
     *total_out = total;
     if (cu[0] != 0 || cu[n] > N) atomicCAS(err, 0, kErrSeqlens);
   }
-  for (int64_t k = i; k < n; k += static_cast<int64_t>(gridDim.x) * blockDim.x)
+  for (int64_t k = i; k < n; k += threads)
     if (cu[k] > cu[k + 1]) atomicCAS(err, 0, kErrSeqlens);
   if (i >= N) return;
   const int r = static_cast<int>(i);
@@ -1733,6 +1799,62 @@ __global__ void __launch_bounds__(256) window_spans_kernel(const int32_t* cu, in
     else hi = mid - 1;
   }
   span[r] = make_int2(max(0, min(cu[lo], r)), min(max(cu[lo + 1], r + 1), total));
+}
+
+__global__ void __launch_bounds__(256) window_spans_kernel(const int32_t* cu, int n, int N, int* total_out, int2* span,
+                                                           int* err) {
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  write_spans(cu, n, N, total_out, span, err, static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x,
+              static_cast<int64_t>(gridDim.x) * blockDim.x);
+}
+
+// Before the backward: the spans (when there are boundaries), and per (KV head, 128-key block) the largest sum|v|
+// of its rows that belong to a sequence, for the powers of two of dS (see the top); row_bound() starts at 0.
+// One CTA a block: half a warp a row, the loads of a warp's 16 rows in flight together.  V is read once, HBM-bound.
+constexpr int PREP_THREADS = 256;
+__global__ void __launch_bounds__(PREP_THREADS) window_prep_kernel(const WinArgs p, const int32_t* cu, int n_seq,
+                                                                   int* total_out, int2* span) {
+  __shared__ float warp_top[PREP_THREADS / 32];
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const int kvh = blockIdx.x % p.Hkv, kb = static_cast<int>(blockIdx.x / p.Hkv);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int shard = kvh / p.kv_t, jl = kvh - shard * p.kv_t;
+  const int total = cu ? max(0, min(cu[n_seq], p.N)) : p.N;
+  const int r0 = kb * BKV + warp * 16 + (lane >> 4);
+  const uint16_t* v = p.QKV + static_cast<int64_t>(shard) * p.N * p.row_w + p.vcol0 + jl * HD + 8 * (lane & 15);
+  uint4 w[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u)
+    w[u] = r0 + 2 * u < total ? *reinterpret_cast<const uint4*>(v + (r0 + 2 * u) * p.row_w) : make_uint4(0u, 0u, 0u, 0u);
+  if (cu && kvh == 0 && threadIdx.x < BKV)
+    write_spans(cu, n_seq, p.N, total_out, span, p.err, static_cast<int64_t>(kb) * BKV + threadIdx.x,
+                static_cast<int64_t>(p.nqb) * BKV);
+  if (kb == 0 && threadIdx.x == 0) *row_bound(p, shard, jl * p.Gs) = 0u;
+  float top = 0.0f;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+    float sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float v0, v1;
+      unpack_f16x2(x[e], v0, v1);
+      sum += fabsf(v0) + fabsf(v1);
+    }
+#pragma unroll
+    for (int m = 8; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    top = fmaxf(top, sum);
+  }
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+  if (lane == 0) warp_top[warp] = top;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int k = 0; k < PREP_THREADS / 32; ++k) top = fmaxf(top, warp_top[k]);
+    *value_bound(p, shard, static_cast<int>(p.vcol0) + jl * HD, kb) = top;
+  }
 }
 
 inline size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -1914,7 +2036,13 @@ tp_status run_window_attn_bwd(const uint16_t* QKV, const uint16_t* O, const uint
     TP_CUDA_CHECK(cudaFuncSetAttribute(window_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, DQ_SMEM));
     configured[dev] = true;
   }
-  TP_RETURN_IF(make_spans(a, o, ws, s));
+  int* total = o.n_seq > 0 ? static_cast<int*>(ws) : nullptr;
+  int2* span = o.n_seq > 0 ? reinterpret_cast<int2*>(static_cast<uint8_t*>(ws) + 256) : nullptr;
+  TP_CUDA_CHECK(launch_pdl(window_prep_kernel, dim3(static_cast<unsigned>(grid_kv)), dim3(PREP_THREADS), 0, s, a,
+                           o.cu_seqlens, static_cast<int>(o.n_seq), total, span));
+  count_launch();
+  a.total = total;
+  a.span = span;
   TP_CUDA_CHECK(launch_pdl(window_dq_kernel, dim3(static_cast<unsigned>(grid_q)), dim3(DQ_THREADS), DQ_SMEM, s, m_qkv,
                            m_do, a));
   count_launch();
