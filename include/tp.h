@@ -541,7 +541,7 @@ tp_status tp_attn_core_backward(const uint16_t* QKV, const tp_bf16* O, const uin
  * taken from the largest |dO| (of 32 rows for dQ, of a KV head for dK) and sum |v|.  Deterministic.  ws:
  * tp_attn_window_backward_workspace_size() bytes, 256-byte aligned (fp32 partial dK, dV of
  * the sinks: 2 KB for each KV head of a shard, sink and chunk of about max(window, 128) rows,
- * 2048 at most; the row spans of cu_seqlens).  Three or four launches.  N == 0 is a no-op. */
+ * 2048 at most, none when window + n_sink >= N, which hides nothing; the row spans of cu_seqlens).  Three or four launches.  N == 0 is a no-op. */
 size_t tp_attn_window_forward_workspace_size(int64_t N, int64_t n_seq);
 tp_status tp_attn_window_forward(const uint16_t* QKV, int64_t N, int64_t d, int n_heads, int n_kv_heads, int head_dim,
                                  int t, int64_t window, int64_t n_sink, float scale, const int32_t* cu_seqlens,

@@ -1878,6 +1878,17 @@ FarPlan far_plan(int64_t N, int Hkv, int64_t W, int64_t S, int64_t n_seq) {
   return f;
 }
 
+// Window and sinks as they act on N rows: neither reaches further, and where they leave no key of N hidden
+// (a hidden key is W back and S from the first) the attention is the full causal one: no sinks then, so
+// no far works and no room for them, however many sinks were asked for.
+struct Reach {
+  int64_t W, S;
+};
+Reach reach_of(int64_t N, int64_t window, int64_t n_sink) {
+  const Reach r{window < N ? window : N, n_sink < N ? n_sink : N};
+  return r.W + r.S >= N ? Reach{N, 0} : r;
+}
+
 tp_status check_window(int64_t N, int64_t d, int n_heads, int n_kv, int head_dim, int t, const WindowAttn& o,
                        AttnShape& sh) {
   if (N < 0 || d < 1 || n_heads < 1 || n_kv < 1 || t < 1 || head_dim < 1) return TP_ERR_INVALID_ARG;
@@ -1897,8 +1908,9 @@ void fill_args(WinArgs& a, int64_t N, int n_heads, int t, const WindowAttn& o, c
   a.Gs = sh.Gs;
   a.kv_t = sh.kv_t;
   a.Hkv = t * sh.kv_t;
-  a.W = static_cast<int>(o.window < N ? o.window : N);
-  a.S = static_cast<int>(o.n_sink < N ? o.n_sink : N);
+  const Reach r = reach_of(N, o.window, o.n_sink);
+  a.W = static_cast<int>(r.W);
+  a.S = static_cast<int>(r.S);
   a.by_head = sh.Gs % 2 == 0;
   a.nqb = static_cast<int>((N + BQ - 1) / BQ);
   a.dt = sh.dt;
@@ -1979,8 +1991,8 @@ size_t window_attn_bwd_ws_bytes(int64_t N, int64_t d, int n_heads, int n_kv, int
                                 int64_t n_sink, int64_t n_seq) {
   AttnShape sh;
   if (N < 0 || window < 1 || n_sink < 0 || n_seq < 0 || !attn_shape(d, n_heads, n_kv, head_dim, t, sh)) return 0;
-  const int64_t W = window < N ? window : N, S = n_sink < N ? n_sink : N;
-  return span_bytes(N, n_seq) + far_plan(N, t * sh.kv_t, W, S, n_seq).bytes;
+  const Reach r = reach_of(N, window, n_sink);
+  return span_bytes(N, n_seq) + far_plan(N, t * sh.kv_t, r.W, r.S, n_seq).bytes;
 }
 
 tp_status run_window_attn_bwd(const uint16_t* QKV, const uint16_t* O, const uint16_t* dO, const float* lse, int64_t N,

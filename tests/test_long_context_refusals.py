@@ -220,3 +220,15 @@ def test_attention_options_name_the_wrong_argument():
                      (dict(pos=torch.zeros(2, 2, dtype=torch.int32)), "pos")]:
         with pytest.raises(ValueError, match=what):
             T.AttentionOptions(**kw)
+
+
+def test_sinks_that_hide_nothing_take_no_workspace():
+    """window + n_sink >= N is full causal attention: no partial sums of sinks, however many there are."""
+    def size(N, W, S, n_seq=0):
+        return L.tp_attn_window_backward_workspace_size(N, 64 * 128, 64, 8, 128, 1, W, S, n_seq)
+    for S in (16384, 10 ** 9, 2 ** 62, 16384 - 1):
+        assert size(16384, 1, S) == 0
+    assert size(16384, 1024, 16384 - 1024) == 0 and size(16384, 1024, 16384) == 0
+    assert size(16384, 1024, 16384, 3) == 256 + 8 * 16384      # the rows' sequences alone
+    assert size(16384, 1, 16382) > 0 and size(16384, 1024, 16384 - 1025) > 0
+    assert size(1, 1, 1) == size(0, 1, 10 ** 9) == 0
