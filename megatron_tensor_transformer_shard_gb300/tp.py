@@ -326,6 +326,14 @@ def _tensor(x, name, dtypes, shape, device, optional=False):
         raise ValueError(f"{name} is on {x.device}, expected {device}")
 
 
+def _buffers(out, device, *expected, optional=()):
+    """Checks a tuple of output buffers, each (name, dtype, shape) of those expected."""
+    if len(out) != len(expected):
+        raise ValueError(f"out: {len(out)} buffers, expected {', '.join(name for name, _, _ in expected)}")
+    for x, (name, dtype, shape) in zip(out, expected):
+        _tensor(x, name + " of out", dtype, shape, device, name in optional)
+
+
 def _on(device, call, *args):
     """call(*args) with `device` current, on its current stream."""
     if torch._C._cuda_getDevice() == device.index:
@@ -552,6 +560,8 @@ def window_decode_attn(Q, K_cache, V_cache, pos, n_kv, window=None, n_sink=0, sc
     _check(not rolling or window is not None, "a rolling cache needs a window")
     if ws is None:
         ws = torch.empty(_decode_ws_bytes(B, n_heads, n_kv, HEAD_DIM, t), dtype=torch.uint8, device=dev)
+    elif ws.device != dev:
+        raise ValueError(f"ws is on {ws.device}, expected {dev}")
     if out is None:
         out = torch.empty(B, n_heads, HEAD_DIM, dtype=BF16, device=dev)
     else:
@@ -632,6 +642,9 @@ def attn_opt_forward(X, Wqkv_p, bqkv_p, Wo_p, b_o, n_heads, n_kv, t, attn, scale
         out = (torch.empty(N, d, dtype=BF16, device=dev), torch.empty(t, N, R, dtype=torch.float16, device=dev),
                torch.empty(t, N, q_t * HEAD_DIM, dtype=BF16, device=dev),
                torch.empty(t, q_t, N, dtype=torch.float32, device=dev))
+    else:
+        _buffers(out, dev, ("Y", BF16, (N, d)), ("QKV", F16, (t, N, R)), ("O", BF16, (t, N, q_t * HEAD_DIM)),
+                 ("lse", torch.float32, (t, q_t, N)))
     Y, QKV, O, lse = out
     raw = torch.empty_like(QKV) if keep_raw and attn.q_gamma is not None else None
     ws = _ws(L.tp_attn_opt_forward_workspace_size(N, d, n_heads, n_kv, HEAD_DIM, t, attn.ptr), dev)
@@ -643,12 +656,13 @@ def attn_opt_forward(X, Wqkv_p, bqkv_p, Wo_p, b_o, n_heads, n_kv, t, attn, scale
 
 def attn_opt_backward(dY, X, QKV_raw, QKV, O, lse, Wqkv_p, Wo_p, n_heads, n_kv, t, attn, scale=None, out=None):
     """Gradients of <Y, dY> of attn_opt_forward: dict of dX, Wqkv_p, bqkv_p, Wo_p, b_o, q_gamma, k_gamma
-    (parameters fp32, packed; the gammas None without norms).  out = (dX, dWqkv, dbqkv, dWo, dbo) buffers."""
+    (parameters fp32, packed; the gammas None without norms).  out = (dX, dWqkv, dbqkv, dWo, dbo) buffers (a
+    bias gradient that is None is left out)."""
     N, d, q_t, R = _block_args(X, Wqkv_p, Wo_p, n_heads, n_kv, t)
     dev = X.device
     f32 = dict(dtype=torch.float32, device=dev)
     _tensor(dY, "dY", BF16, (N, d), dev)
-    _tensor(QKV_raw, "QKV_raw", F16, (t, N, R), dev, True)
+    _tensor(QKV_raw, "QKV_raw", F16, (t, N, R), dev, attn.q_gamma is None)
     _tensor(QKV, "QKV", F16, (t, N, R), dev)
     _tensor(O, "O", BF16, (t, N, q_t * HEAD_DIM), dev)
     _tensor(lse, "lse", torch.float32, (t, q_t, N), dev)
@@ -656,6 +670,10 @@ def attn_opt_backward(dY, X, QKV_raw, QKV, O, lse, Wqkv_p, Wo_p, n_heads, n_kv, 
     if out is None:
         out = (torch.empty(N, d, dtype=BF16, device=dev), torch.empty(Wqkv_p.shape, **f32),
                torch.empty(Wqkv_p.shape[:2], **f32), torch.empty(Wo_p.shape, **f32), torch.empty(d, **f32))
+    else:
+        _buffers(out, dev, ("dX", BF16, (N, d)), ("dWqkv", torch.float32, Wqkv_p.shape),
+                 ("dbqkv", torch.float32, Wqkv_p.shape[:2]), ("dWo", torch.float32, Wo_p.shape),
+                 ("dbo", torch.float32, (d,)), optional=("dbqkv", "dbo"))
     dX, dWqkv, dbqkv, dWo, dbo = out
     dqg = dkg = None
     if attn.q_gamma is not None:
@@ -682,7 +700,12 @@ def _decode_attn_opt(x, w, K_cache, V_cache, pos, scale, ws, out, attn):
     attn.check(dev)
     if ws is None:
         ws = decode_attn_opt_workspace(B, w, dev)
-    y = out if out is not None else torch.empty(B, w.d, dtype=BF16, device=dev)
+    elif ws.device != dev:
+        raise ValueError(f"ws is on {ws.device}, expected {dev}")
+    if out is None:
+        out = torch.empty(B, w.d, dtype=BF16, device=dev)
+    else:
+        _tensor(out, "out", BF16, (B, w.d), dev)
     _on(dev, L.tp_decode_attn_opt_forward, x, B, w.d, w.n_heads, w.n_kv, w.head_dim, w.t, scale, attn.ptr, w.Wqkv_p,
-        w.bqkv_p, w.Wo_p, w.b_o, K_cache, V_cache, L_max, pos, y, ws, ws.numel())
-    return y
+        w.bqkv_p, w.Wo_p, w.b_o, K_cache, V_cache, L_max, pos, out, ws, ws.numel())
+    return out

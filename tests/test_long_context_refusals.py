@@ -232,3 +232,47 @@ def test_sinks_that_hide_nothing_take_no_workspace():
     assert size(16384, 1024, 16384, 3) == 256 + 8 * 16384      # the rows' sequences alone
     assert size(16384, 1, 16382) > 0 and size(16384, 1024, 16384 - 1025) > 0
     assert size(1, 1, 1) == size(0, 1, 10 ** 9) == 0
+
+
+def test_blocks_check_the_buffers_of_out():
+    """A short, wrongly typed or missing buffer is named before anything is launched."""
+    import types
+    bf, N, d = torch.bfloat16, 6, 512
+    X, W, Wo = torch.zeros(N, d, dtype=bf), torch.zeros(1, 1024, d, dtype=bf), torch.zeros(1, d, 512, dtype=bf)
+    opt = T.AttentionOptions(4)
+    good = dict(Y=torch.zeros(N, d, dtype=bf), QKV=torch.zeros(1, N, 1024, dtype=torch.float16),
+                O=torch.zeros(1, N, 512, dtype=bf), lse=torch.zeros(1, 4, N))
+
+    def fwd_(**kw):
+        with pytest.raises(ValueError) as e:
+            T.attn_opt_forward(X, W, None, Wo, None, 4, 2, 1, opt, out=tuple({**good, **kw}.values()))
+        return str(e.value)
+    for kw in (dict(Y=good["Y"][:5]), dict(Y=good["Y"].half()), dict(Y=None), dict(QKV=good["QKV"].bfloat16()),
+               dict(QKV=good["QKV"][:, :, :512]), dict(O=torch.zeros(1, N, 256, dtype=bf)), dict(lse=good["lse"].half()),
+               dict(lse=torch.zeros(4, N))):
+        assert f"{next(iter(kw))} of out" in fwd_(**kw)
+    assert "buffers" in fwd_(more=good["Y"])
+    grads = dict(dX=good["Y"], dWqkv=torch.zeros(1, 1024, d), dbqkv=torch.zeros(1, 1024), dWo=torch.zeros(1, d, 512),
+                 dbo=torch.zeros(d))
+
+    def bwd(attn=opt, raw=None, **kw):
+        with pytest.raises(ValueError) as e:
+            T.attn_opt_backward(X, X, raw, good["QKV"], good["O"], good["lse"], W, Wo, 4, 2, 1, attn,
+                                out=tuple({**grads, **kw}.values()))
+        return str(e.value)
+    for kw in (dict(dX=X.float()), dict(dWqkv=grads["dWqkv"][:, :512]), dict(dWqkv=W), dict(dbqkv=torch.zeros(512)),
+               dict(dWo=torch.zeros(d, 512)), dict(dbo=torch.zeros(4)), dict(dX=None)):
+        assert f"{next(iter(kw))} of out" in bwd(**kw)
+    g = torch.ones(128, dtype=bf)
+    assert "QKV_raw" in bwd(T.AttentionOptions(4, q_gamma=g, k_gamma=g))
+    w = types.SimpleNamespace(t=1, kv_t=2, d=d, n_heads=4, n_kv=2, head_dim=128)
+    cache = torch.zeros(1, 2, 3, 8, 128, dtype=torch.float16)
+    for out in (torch.zeros(2, d, dtype=bf), torch.zeros(3, d), torch.zeros(3, 2 * d, dtype=bf)[:, ::2]):
+        with pytest.raises(ValueError, match="out"):
+            T.decode_attn_forward(X[:3], w, cache, cache.clone(), torch.zeros(3, dtype=torch.int32), attn=opt, out=out)
+    ws = torch.zeros(64, dtype=torch.uint8, device="meta")
+    with pytest.raises(ValueError, match="ws is on"):
+        T.decode_attn_forward(X[:3], w, cache, cache.clone(), torch.zeros(3, dtype=torch.int32), attn=opt, ws=ws)
+    with pytest.raises(ValueError, match="ws is on"):
+        T.window_decode_attn(torch.zeros(3, 4, 128, dtype=torch.float16), cache, cache.clone(),
+                             torch.zeros(3, dtype=torch.int32), 2, 4, ws=ws)
