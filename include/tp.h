@@ -601,7 +601,9 @@ typedef struct tp_attn_options {
  * Backward: tp_attn_gqa_backward with the same `opt`; QKV_raw is required with norms.
  * dq_gamma, dk_gamma [128] fp32 (nullable; only with norms) follow `accumulate`.  X and dY in
  * rows of no sequence must be finite; dQKV is 0 there, and dO is not used.  ws:
- * tp_attn_opt_backward_workspace_size() bytes, 256-byte aligned. */
+ * tp_attn_opt_backward_workspace_size() bytes, 256-byte aligned, over none of the inputs or dX
+ * (TP_ERR_INVALID_ARG).  What the operators between the projections refuse is refused before
+ * anything is launched. */
 size_t tp_attn_opt_forward_workspace_size(int64_t N, int64_t d, int n_heads, int n_kv_heads, int head_dim, int t,
                                           const tp_attn_options* opt);
 tp_status tp_attn_opt_forward(const tp_bf16* X, int64_t N, int64_t d, int n_heads, int n_kv_heads, int head_dim, int t,

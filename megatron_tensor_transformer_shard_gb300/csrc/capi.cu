@@ -340,6 +340,22 @@ tp_status attn_backward_block(const tp_bf16* dY, const tp_bf16* X, const uint16_
     }
     return TP_OK;
   }
+  QkNormRope nr;
+  if (o) {  // what the steps behind the first GEMM would refuse, and a workspace over what is read or kept
+    nr = norm_rope_of(*o);
+    if (f16in) nr.flags |= TP_QKNR_F16_GRAD;
+    TP_RETURN_IF(window_attn_bwd_ok(QKV_save, O_save, w.dO, lse_save, N, d, n_heads, n_kv_heads, head_dim, t,
+                                    window_of(*o, N), w.Dvec, w.dQKV, ow.win, ow.win_bytes));
+    if (o->inv_freq || o->q_gamma)
+      TP_RETURN_IF(qk_norm_rope_bwd_ok(w.dQKV, QKV_raw, N, n_heads, n_kv_heads, head_dim, t, nr, w.dQKV, dq_gamma,
+                                       dk_gamma, ow.norm, ow.norm_bytes));
+    const size_t x_bytes = static_cast<size_t>(N) * d * 2, qkv_bytes = static_cast<size_t>(t) * N * rw * 2;
+    const size_t lse_bytes = static_cast<size_t>(n_heads) * N * 4;
+    if (overlap(ws, ow.total, dY, x_bytes) || overlap(ws, ow.total, X, x_bytes) || overlap(ws, ow.total, dX, x_bytes) ||
+        overlap(ws, ow.total, QKV_save, qkv_bytes) || overlap(ws, ow.total, O_save, x_bytes) ||
+        overlap(ws, ow.total, lse_save, lse_bytes) || (QKV_raw && overlap(ws, ow.total, QKV_raw, qkv_bytes)))
+      return TP_ERR_INVALID_ARG;
+  }
   // dO_i = dY W_o,i^T  (row-parallel W_o, input grad stays sharded).
   GemmProblem g;
   g.M = N; g.N = dt; g.K = d; g.nbatch = t;
@@ -364,12 +380,9 @@ tp_status attn_backward_block(const tp_bf16* dY, const tp_bf16* X, const uint16_
   } else {
     TP_RETURN_IF(run_window_attn_bwd(QKV_save, O_save, w.dO, lse_save, N, d, n_heads, n_kv_heads, head_dim, t,
                                      window_of(*o, N), scale, w.Dvec, w.dQKV, f16in, ow.win, ow.win_bytes, s));
-    if (o->inv_freq || o->q_gamma) {  // dQKV of the projection, in place
-      QkNormRope q = norm_rope_of(*o);
-      if (f16in) q.flags |= TP_QKNR_F16_GRAD;
-      TP_RETURN_IF(run_qk_norm_rope_bwd(w.dQKV, QKV_raw, N, n_heads, n_kv_heads, head_dim, t, q, w.dQKV, dq_gamma,
+    if (o->inv_freq || o->q_gamma)  // dQKV of the projection, in place
+      TP_RETURN_IF(run_qk_norm_rope_bwd(w.dQKV, QKV_raw, N, n_heads, n_kv_heads, head_dim, t, nr, w.dQKV, dq_gamma,
                                         dk_gamma, accumulate, ow.norm, ow.norm_bytes, s));
-    }
   }
   // Bias gradients in one fused pass: db_o once (g backward is the identity), db_qkv per shard.
   if (dbo || dbqkv_p) {
@@ -419,6 +432,14 @@ tp_status attn_forward_block(const tp_bf16* X, int64_t N, int64_t d, int n_heads
   if (!gqa_ok(d, n_heads, n_kv_heads, head_dim, t)) return TP_ERR_SHAPE;
   if (N == 0) return TP_OK;
   if (!X || !Wqkv_p || !Wo_p || !Y || !QKV_save || !O_save || !lse_save) return TP_ERR_INVALID_ARG;
+  const size_t base = o ? round_up(window_attn_fwd_ws_bytes(N, o->n_seq), 256) : 0;  // the required part
+  if (o) {  // what the steps behind the projection would refuse
+    if (o->inv_freq || o->q_gamma)
+      TP_RETURN_IF(qk_norm_rope_fwd_ok(QKV_raw ? QKV_raw : QKV_save, N, n_heads, n_kv_heads, head_dim, t, norm_rope_of(*o),
+                                       QKV_save));
+    TP_RETURN_IF(window_attn_fwd_ok(QKV_save, N, d, n_heads, n_kv_heads, head_dim, t, window_of(*o, N), O_save, lse_save,
+                                    ws, base));
+  }
   // f (identity) + column-parallel W_qkv by KV group: QKV_i = X W_qkv,i + b_qkv,i, stored fp16.
   const int64_t rw = qkv_row_width(n_heads, n_kv_heads, head_dim, t);
   GemmProblem c;
@@ -429,7 +450,6 @@ tp_status attn_forward_block(const tp_bf16* X, int64_t N, int64_t d, int n_heads
   c.f16_ab = (flags & TP_ATTN_F16_INPUT) ? 1 : 0;  // X and W_qkv in IEEE fp16
   c.d = nullptr; c.d2 = QKV_raw ? QKV_raw : QKV_save; c.ldd = rw; c.d_batch_stride = N * rw;
   c.bias = bqkv_p; c.bias_batch_stride = rw;
-  const size_t base = o ? round_up(window_attn_fwd_ws_bytes(N, o->n_seq), 256) : 0;  // the required part
   size_t sk_bytes = 0;
   void* sk_ws = sk_part_of(ws, ws_bytes, base, &sk_bytes);  // optional: the GEMMs' split-K partials
   c.sk_ws = sk_ws; c.sk_ws_bytes = sk_bytes;

@@ -1037,17 +1037,14 @@ size_t window_decode_ws_bytes(int64_t B, int n_heads, int n_kv, int head_dim, in
   return window_ws_layout(nullptr, sh).bytes;
 }
 
-tp_status run_window_decode(const uint16_t* Q, int64_t B, int n_heads, int n_kv, int head_dim, int t, int64_t window,
-                            int64_t n_sink, int rolling, float scale, const uint16_t* Kc, const uint16_t* Vc,
-                            int64_t L_max, const int32_t* pos, uint16_t* O, void* ws, size_t ws_bytes, cudaStream_t s) {
+tp_status window_decode_ok(const uint16_t* Q, int64_t B, int n_heads, int n_kv, int head_dim, int t, int64_t window,
+                           int64_t n_sink, int rolling, const uint16_t* Kc, const uint16_t* Vc, int64_t L_max,
+                           const int32_t* pos, const uint16_t* O, const void* ws, size_t ws_bytes) {
   if (B < 0 || L_max < 1 || window < 1 || n_sink < 0) return TP_ERR_INVALID_ARG;
   DecShape sh;
   if (!decode_shape(B, n_heads, n_kv, head_dim, t, sh)) return TP_ERR_SHAPE;
   if (L_max > (1LL << 30)) return TP_ERR_SHAPE;
   if (rolling && (window > L_max || n_sink > L_max || n_sink + window > L_max)) return TP_ERR_SHAPE;
-  // nothing lies beyond the cache: both fit 32 bits
-  if (window > L_max) window = L_max;
-  if (n_sink > L_max) n_sink = L_max;
   // the tile list is indexed in 32 bits, times the grid (a cache of 2^24 tiles has 2^40 bytes)
   if (static_cast<int64_t>(sh.S) * ((L_max + BK - 1) / BK + 1) >= (1LL << 24)) return TP_ERR_SHAPE;
   if (B == 0) return TP_OK;
@@ -1055,8 +1052,22 @@ tp_status run_window_decode(const uint16_t* Q, int64_t B, int n_heads, int n_kv,
   if (!aligned16(Q) || !aligned16(Kc) || !aligned16(Vc) || !aligned16(O) || (reinterpret_cast<uintptr_t>(pos) & 3u) != 0 ||
       (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
     return TP_ERR_ALIGN;
+  if (!ws || ws_bytes < window_ws_layout(nullptr, sh).bytes) return TP_ERR_WORKSPACE;
+  return TP_OK;
+}
+
+tp_status run_window_decode(const uint16_t* Q, int64_t B, int n_heads, int n_kv, int head_dim, int t, int64_t window,
+                            int64_t n_sink, int rolling, float scale, const uint16_t* Kc, const uint16_t* Vc,
+                            int64_t L_max, const int32_t* pos, uint16_t* O, void* ws, size_t ws_bytes, cudaStream_t s) {
+  TP_RETURN_IF(window_decode_ok(Q, B, n_heads, n_kv, head_dim, t, window, n_sink, rolling, Kc, Vc, L_max, pos, O, ws,
+                                ws_bytes));
+  if (B == 0) return TP_OK;
+  DecShape sh;
+  if (!decode_shape(B, n_heads, n_kv, head_dim, t, sh)) return TP_ERR_SHAPE;
+  // nothing lies beyond the cache: both fit 32 bits
+  if (window > L_max) window = L_max;
+  if (n_sink > L_max) n_sink = L_max;
   const WinWs w = window_ws_layout(ws, sh);
-  if (!ws || ws_bytes < w.bytes) return TP_ERR_WORKSPACE;
   TP_RETURN_IF(ready());
   CUtensorMap mk, mv, mq;
   const uint64_t S = static_cast<uint64_t>(sh.S);
@@ -1141,11 +1152,11 @@ tp_status run_decode_opt(const uint16_t* x, int64_t B, int64_t d, int n_heads, i
   if (window == 0) window = L_max;
   QkNormRope nr = norm_rope;
   nr.pos = pos;
-  // the checks of both operators (no rows: nothing runs), before anything is launched
-  TP_RETURN_IF(run_qk_norm_rope_append(nullptr, 0, n_heads, n_kv, head_dim, t, nr, nullptr, nullptr, nullptr, L_max, window,
-                                       n_sink, rolling, s, 1));
-  TP_RETURN_IF(run_window_decode(nullptr, 0, n_heads, n_kv, head_dim, t, window, n_sink, rolling, scale, nullptr, nullptr,
-                                 L_max, nullptr, nullptr, nullptr, 0, s));
+  // both operators' checks, before anything is launched: of the sizes (no rows, so no pointers yet) ..
+  TP_RETURN_IF(qk_norm_rope_append_ok(nullptr, 0, n_heads, n_kv, head_dim, t, nr, nullptr, nullptr, nullptr, L_max, window,
+                                      n_sink, rolling, 1));
+  TP_RETURN_IF(window_decode_ok(nullptr, 0, n_heads, n_kv, head_dim, t, window, n_sink, rolling, nullptr, nullptr, L_max,
+                                nullptr, nullptr, nullptr, 0));
   if (static_cast<int64_t>(sh.S) * ((L_max + BK - 1) / BK + 1) >= (1LL << 24)) return TP_ERR_SHAPE;
   if (B == 0) return TP_OK;
   if (!x || !Wqkv_p || !Wo_p || !Kc || !Vc || !pos || !y || !ws) return TP_ERR_INVALID_ARG;
@@ -1154,6 +1165,11 @@ tp_status run_decode_opt(const uint16_t* x, int64_t B, int64_t d, int n_heads, i
     return TP_ERR_ALIGN;
   const OptWs w = opt_ws_layout(ws, B, d, n_heads, t, sh);
   if (ws_bytes < w.bytes) return TP_ERR_WORKSPACE;
+  // .. and of the pointers
+  TP_RETURN_IF(qk_norm_rope_append_ok(w.rows, B, n_heads, n_kv, head_dim, t, nr, w.q, Kc, Vc, L_max, window, n_sink,
+                                      rolling, 1));
+  TP_RETURN_IF(window_decode_ok(w.q, B, n_heads, n_kv, head_dim, t, window, n_sink, rolling, Kc, Vc, L_max, pos, w.O,
+                                w.core, w.core_bytes));
   TP_RETURN_IF(ready());
   const int64_t nq = static_cast<int64_t>(n_heads) * HD;
   // The rows before norm and rotation are fp16, as the caches and the prompt's block hold them: a token that is

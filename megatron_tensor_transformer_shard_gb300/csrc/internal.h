@@ -254,6 +254,15 @@ tp_status run_qk_norm_rope_append(const uint16_t* QKV, int64_t B, int n_heads, i
                                   const QkNormRope& o, uint16_t* Q, uint16_t* Kc, uint16_t* Vc, int64_t L_max,
                                   int64_t window, int64_t n_sink, int rolling, cudaStream_t s, int token_major = 0);
 size_t qk_norm_rope_bwd_ws_bytes();
+// .._ok: all that the call would be refused for, for callers that launch something before it.
+tp_status qk_norm_rope_fwd_ok(const uint16_t* QKV, int64_t N, int n_heads, int n_kv, int head_dim, int t,
+                              const QkNormRope& o, const uint16_t* out);
+tp_status qk_norm_rope_append_ok(const uint16_t* QKV, int64_t B, int n_heads, int n_kv, int head_dim, int t,
+                                 const QkNormRope& o, const uint16_t* Q, const uint16_t* Kc, const uint16_t* Vc,
+                                 int64_t L_max, int64_t window, int64_t n_sink, int rolling, int token_major);
+tp_status qk_norm_rope_bwd_ok(const uint16_t* dQKV, const uint16_t* QKV, int64_t N, int n_heads, int n_kv, int head_dim,
+                              int t, const QkNormRope& o, const uint16_t* out, const float* dq_gamma,
+                              const float* dk_gamma, const void* ws, size_t ws_bytes);
 tp_status run_qk_norm_rope_bwd(const uint16_t* dQKV, const uint16_t* QKV, int64_t N, int n_heads, int n_kv, int head_dim,
                                int t, const QkNormRope& o, uint16_t* out, float* dq_gamma, float* dk_gamma,
                                int accumulate, void* ws, size_t ws_bytes, cudaStream_t s);
@@ -265,6 +274,9 @@ tp_status run_decode_attn(const uint16_t* x, int64_t B, int64_t d, int n_heads, 
                           const uint16_t* bo, uint16_t* Kc, uint16_t* Vc, int64_t L_max, const int32_t* pos,
                           uint16_t* y, void* ws, size_t ws_bytes, cudaStream_t s);
 size_t window_decode_ws_bytes(int64_t B, int n_heads, int n_kv, int head_dim, int t);
+tp_status window_decode_ok(const uint16_t* Q, int64_t B, int n_heads, int n_kv, int head_dim, int t, int64_t window,
+                           int64_t n_sink, int rolling, const uint16_t* Kc, const uint16_t* Vc, int64_t L_max,
+                           const int32_t* pos, const uint16_t* O, const void* ws, size_t ws_bytes);
 tp_status run_window_decode(const uint16_t* Q, int64_t B, int n_heads, int n_kv, int head_dim, int t, int64_t window,
                             int64_t n_sink, int rolling, float scale, const uint16_t* Kc, const uint16_t* Vc,
                             int64_t L_max, const int32_t* pos, uint16_t* O, void* ws, size_t ws_bytes, cudaStream_t s);
@@ -310,6 +322,11 @@ struct WindowAttn {
   int64_t n_seq = 0;
 };
 size_t window_attn_fwd_ws_bytes(int64_t N, int64_t n_seq);
+tp_status window_attn_fwd_ok(const uint16_t* QKV, int64_t N, int64_t d, int n_heads, int n_kv, int head_dim, int t,
+                             const WindowAttn& o, const uint16_t* O, const float* lse, const void* ws, size_t ws_bytes);
+tp_status window_attn_bwd_ok(const uint16_t* QKV, const uint16_t* O, const uint16_t* dO, const float* lse, int64_t N,
+                             int64_t d, int n_heads, int n_kv, int head_dim, int t, const WindowAttn& o,
+                             const float* Dvec, const uint16_t* dQKV, const void* ws, size_t ws_bytes);
 // zero_pad: rows behind the last sequence get O = 0, lse = 0 (else they keep what they hold).
 tp_status run_window_attn_fwd(const uint16_t* QKV, int64_t N, int64_t d, int n_heads, int n_kv, int head_dim, int t,
                               const WindowAttn& o, float scale, uint16_t* O, float* lse, int zero_pad, void* ws,

@@ -750,19 +750,91 @@ tp_status check_common(const QkNormRope& o, int64_t N, int n_heads, int n_kv, in
 // Ranges that share bytes without being the same range (in place is fine, partly over is not).
 bool partly_over(const void* p, const void* q, size_t bytes) { return p != q && overlap(p, bytes, q, bytes); }
 
-}  // namespace
-
-tp_status run_qk_norm_rope_fwd(const uint16_t* QKV, int64_t N, int n_heads, int n_kv, int head_dim, int t,
-                               const QkNormRope& o, uint16_t* out, cudaStream_t s) {
-  QkArgs a{};
-  int rot;
-  bool norm;
+// All that a call can be refused for, before anything is launched; fills the shape fields of `a`.
+tp_status check_fwd(const uint16_t* QKV, int64_t N, int n_heads, int n_kv, int head_dim, int t, const QkNormRope& o,
+                    const uint16_t* out, QkArgs& a, int& rot, bool& norm) {
   TP_RETURN_IF(check_common(o, N, n_heads, n_kv, head_dim, t, a, rot, norm));
   if (o.flags & TP_QKNR_F16_GRAD) return TP_ERR_UNSUPPORTED;
   if (N == 0) return TP_OK;
   if (!QKV || !out) return TP_ERR_INVALID_ARG;
   if (!aligned16(QKV) || !aligned16(out)) return TP_ERR_ALIGN;
   if (partly_over(QKV, out, static_cast<size_t>(a.rows) * a.R * 2)) return TP_ERR_INVALID_ARG;
+  return TP_OK;
+}
+
+tp_status check_append(const uint16_t* QKV, int64_t B, int n_heads, int n_kv, int head_dim, int t, const QkNormRope& o,
+                       const uint16_t* Q, const uint16_t* Kc, const uint16_t* Vc, int64_t L_max, int64_t window,
+                       int64_t n_sink, int rolling, int token_major, QkArgs& a, int& rot, bool& norm) {
+  TP_RETURN_IF(check_common(o, B, n_heads, n_kv, head_dim, t, a, rot, norm, token_major != 0));
+  if (o.flags & TP_QKNR_F16_GRAD) return TP_ERR_UNSUPPORTED;
+  if (L_max < 1 || (rolling && (window < 1 || n_sink < 0))) return TP_ERR_INVALID_ARG;
+  if (L_max > (1LL << 30)) return TP_ERR_SHAPE;
+  if (rolling && (window > L_max || n_sink > L_max || n_sink + window > L_max)) return TP_ERR_SHAPE;
+  if (B == 0) return TP_OK;
+  if (!QKV || !Q || !Kc || !Vc || !o.pos) return TP_ERR_INVALID_ARG;
+  if (!aligned16(QKV) || !aligned16(Q) || !aligned16(Kc) || !aligned16(Vc)) return TP_ERR_ALIGN;
+  const size_t cache = static_cast<size_t>(t) * a.kv_t * B * L_max * HD * 2;
+  const size_t qb = static_cast<size_t>(B) * n_heads * HD * 2;
+  const size_t xb = static_cast<size_t>(a.rows) * a.R * 2;
+  if (overlap(Kc, cache, Vc, cache) || overlap(Q, qb, Kc, cache) || overlap(Q, qb, Vc, cache) ||
+      overlap(QKV, xb, Q, qb) || overlap(QKV, xb, Kc, cache) || overlap(QKV, xb, Vc, cache))
+    return TP_ERR_INVALID_ARG;
+  return TP_OK;
+}
+
+tp_status check_bwd(const uint16_t* dQKV, const uint16_t* QKV, int64_t N, int n_heads, int n_kv, int head_dim, int t,
+                    const QkNormRope& o, const uint16_t* out, const float* dq_gamma, const float* dk_gamma, const void* ws,
+                    size_t ws_bytes, QkArgs& a, int& rot, bool& norm) {
+  TP_RETURN_IF(check_common(o, N, n_heads, n_kv, head_dim, t, a, rot, norm));
+  if (!norm && (dq_gamma || dk_gamma)) return TP_ERR_INVALID_ARG;
+  if (N == 0) return TP_OK;
+  if (!dQKV || !out || (norm && !QKV)) return TP_ERR_INVALID_ARG;
+  if (!aligned16(dQKV) || !aligned16(QKV) || !aligned16(out)) return TP_ERR_ALIGN;
+  const size_t bytes = static_cast<size_t>(a.rows) * a.R * 2;
+  if (partly_over(dQKV, out, bytes) || (norm && (QKV == out || partly_over(QKV, out, bytes)))) return TP_ERR_INVALID_ARG;
+  if (norm && (!ws || ws_bytes < qk_norm_rope_bwd_ws_bytes())) return TP_ERR_WORKSPACE;
+  if (norm && !aligned16(ws)) return TP_ERR_ALIGN;
+  return TP_OK;
+}
+
+}  // namespace
+
+size_t qk_norm_rope_bwd_ws_bytes() { return static_cast<size_t>(BWD_MAX_GRID) * 2 * HD * sizeof(float); }
+
+tp_status qk_norm_rope_fwd_ok(const uint16_t* QKV, int64_t N, int n_heads, int n_kv, int head_dim, int t,
+                              const QkNormRope& o, const uint16_t* out) {
+  QkArgs a{};
+  int rot;
+  bool norm;
+  return check_fwd(QKV, N, n_heads, n_kv, head_dim, t, o, out, a, rot, norm);
+}
+
+tp_status qk_norm_rope_append_ok(const uint16_t* QKV, int64_t B, int n_heads, int n_kv, int head_dim, int t,
+                                 const QkNormRope& o, const uint16_t* Q, const uint16_t* Kc, const uint16_t* Vc,
+                                 int64_t L_max, int64_t window, int64_t n_sink, int rolling, int token_major) {
+  QkArgs a{};
+  int rot;
+  bool norm;
+  return check_append(QKV, B, n_heads, n_kv, head_dim, t, o, Q, Kc, Vc, L_max, window, n_sink, rolling, token_major, a,
+                      rot, norm);
+}
+
+tp_status qk_norm_rope_bwd_ok(const uint16_t* dQKV, const uint16_t* QKV, int64_t N, int n_heads, int n_kv, int head_dim,
+                              int t, const QkNormRope& o, const uint16_t* out, const float* dq_gamma,
+                              const float* dk_gamma, const void* ws, size_t ws_bytes) {
+  QkArgs a{};
+  int rot;
+  bool norm;
+  return check_bwd(dQKV, QKV, N, n_heads, n_kv, head_dim, t, o, out, dq_gamma, dk_gamma, ws, ws_bytes, a, rot, norm);
+}
+
+tp_status run_qk_norm_rope_fwd(const uint16_t* QKV, int64_t N, int n_heads, int n_kv, int head_dim, int t,
+                               const QkNormRope& o, uint16_t* out, cudaStream_t s) {
+  QkArgs a{};
+  int rot;
+  bool norm;
+  TP_RETURN_IF(check_fwd(QKV, N, n_heads, n_kv, head_dim, t, o, out, a, rot, norm));
+  if (N == 0) return TP_OK;
   TP_RETURN_IF(ready());
   const bool bf16 = (o.flags & TP_QKNR_BF16_INPUT) != 0;
   if (QKV == out && !bf16) a.nh = a.q_t + a.kv_t;  // in place: V stays as it is
@@ -780,20 +852,9 @@ tp_status run_qk_norm_rope_append(const uint16_t* QKV, int64_t B, int n_heads, i
   QkArgs a{};
   int rot;
   bool norm;
-  TP_RETURN_IF(check_common(o, B, n_heads, n_kv, head_dim, t, a, rot, norm, token_major != 0));
-  if (o.flags & TP_QKNR_F16_GRAD) return TP_ERR_UNSUPPORTED;
-  if (L_max < 1 || (rolling && (window < 1 || n_sink < 0))) return TP_ERR_INVALID_ARG;
-  if (L_max > (1LL << 30)) return TP_ERR_SHAPE;
-  if (rolling && (window > L_max || n_sink > L_max || n_sink + window > L_max)) return TP_ERR_SHAPE;
+  TP_RETURN_IF(check_append(QKV, B, n_heads, n_kv, head_dim, t, o, Q, Kc, Vc, L_max, window, n_sink, rolling, token_major,
+                            a, rot, norm));
   if (B == 0) return TP_OK;
-  if (!QKV || !Q || !Kc || !Vc || !o.pos) return TP_ERR_INVALID_ARG;
-  if (!aligned16(QKV) || !aligned16(Q) || !aligned16(Kc) || !aligned16(Vc)) return TP_ERR_ALIGN;
-  const size_t cache = static_cast<size_t>(t) * a.kv_t * B * L_max * HD * 2;
-  const size_t qb = static_cast<size_t>(B) * n_heads * HD * 2;
-  const size_t xb = static_cast<size_t>(a.rows) * a.R * 2;
-  if (overlap(Kc, cache, Vc, cache) || overlap(Q, qb, Kc, cache) || overlap(Q, qb, Vc, cache) ||
-      overlap(QKV, xb, Q, qb) || overlap(QKV, xb, Kc, cache) || overlap(QKV, xb, Vc, cache))
-    return TP_ERR_INVALID_ARG;
   TP_RETURN_IF(ready());
   a.x = QKV;
   a.x_shard = token_major ? a.R : B * a.R;
@@ -812,31 +873,22 @@ tp_status run_qk_norm_rope_append(const uint16_t* QKV, int64_t B, int n_heads, i
                                         : launch_append<false>(a, rot, norm, grid, s);
 }
 
-size_t qk_norm_rope_bwd_ws_bytes() { return static_cast<size_t>(BWD_MAX_GRID) * 2 * HD * sizeof(float); }
-
 tp_status run_qk_norm_rope_bwd(const uint16_t* dQKV, const uint16_t* QKV, int64_t N, int n_heads, int n_kv, int head_dim,
                                int t, const QkNormRope& o, uint16_t* out, float* dq_gamma, float* dk_gamma,
                                int accumulate, void* ws, size_t ws_bytes, cudaStream_t s) {
   QkArgs a{};
   int rot;
   bool norm;
-  TP_RETURN_IF(check_common(o, N, n_heads, n_kv, head_dim, t, a, rot, norm));
-  if (!norm && (dq_gamma || dk_gamma)) return TP_ERR_INVALID_ARG;
+  TP_RETURN_IF(check_bwd(dQKV, QKV, N, n_heads, n_kv, head_dim, t, o, out, dq_gamma, dk_gamma, ws, ws_bytes, a, rot,
+                         norm));
+  TP_RETURN_IF(ready());
   if (N == 0) {
-    TP_RETURN_IF(ready());
     if (!accumulate) {
       if (dq_gamma) TP_CUDA_CHECK(cudaMemsetAsync(dq_gamma, 0, HD * sizeof(float), s));
       if (dk_gamma) TP_CUDA_CHECK(cudaMemsetAsync(dk_gamma, 0, HD * sizeof(float), s));
     }
     return TP_OK;
   }
-  if (!dQKV || !out || (norm && !QKV)) return TP_ERR_INVALID_ARG;
-  if (!aligned16(dQKV) || !aligned16(QKV) || !aligned16(out)) return TP_ERR_ALIGN;
-  const size_t bytes = static_cast<size_t>(a.rows) * a.R * 2;
-  if (partly_over(dQKV, out, bytes) || (norm && (QKV == out || partly_over(QKV, out, bytes)))) return TP_ERR_INVALID_ARG;
-  if (norm && (!ws || ws_bytes < qk_norm_rope_bwd_ws_bytes())) return TP_ERR_WORKSPACE;
-  if (norm && !aligned16(ws)) return TP_ERR_ALIGN;
-  TP_RETURN_IF(ready());
   if (dQKV == out) a.nh = a.q_t + a.kv_t;  // in place: dV stays as it is
   a.x = QKV;
   a.dy = dQKV;

@@ -1901,6 +1901,19 @@ tp_status check_window(int64_t N, int64_t d, int n_heads, int n_kv, int head_dim
   return TP_OK;
 }
 
+// Pairs of query tiles of the forward, and works of the two backward kernels.
+int64_t fwd_works(int64_t N, int n_heads, const AttnShape& sh) {
+  const int64_t nqb = (N + BQ - 1) / BQ;
+  return sh.Gs % 2 == 0 ? n_heads / 2 * nqb : n_heads * ((nqb + 1) / 2);
+}
+struct BwdWorks {
+  int64_t q, kv, far;
+};
+BwdWorks bwd_works(int64_t N, int n_heads, int Hkv, const FarPlan& f) {
+  const int64_t nqb = (N + BQ - 1) / BQ;
+  return BwdWorks{n_heads * nqb, Hkv * nqb, static_cast<int64_t>(Hkv) * f.nch * f.nsb};
+}
+
 void fill_args(WinArgs& a, int64_t N, int n_heads, int t, const WindowAttn& o, const AttnShape& sh, float scale) {
   a.N = static_cast<int>(N);
   a.H = n_heads;
@@ -1939,9 +1952,8 @@ tp_status make_spans(WinArgs& a, const WindowAttn& o, void* ws, cudaStream_t s) 
 
 size_t window_attn_fwd_ws_bytes(int64_t N, int64_t n_seq) { return N < 0 || n_seq < 0 ? 0 : span_bytes(N, n_seq); }
 
-tp_status run_window_attn_fwd(const uint16_t* QKV, int64_t N, int64_t d, int n_heads, int n_kv, int head_dim, int t,
-                              const WindowAttn& o, float scale, uint16_t* O, float* lse, int zero_pad, void* ws,
-                              size_t ws_bytes, cudaStream_t s) {
+tp_status window_attn_fwd_ok(const uint16_t* QKV, int64_t N, int64_t d, int n_heads, int n_kv, int head_dim, int t,
+                             const WindowAttn& o, const uint16_t* O, const float* lse, const void* ws, size_t ws_bytes) {
   AttnShape sh;
   TP_RETURN_IF(check_window(N, d, n_heads, n_kv, head_dim, t, o, sh));
   if (N == 0) return TP_OK;
@@ -1956,11 +1968,19 @@ tp_status run_window_attn_fwd(const uint16_t* QKV, int64_t N, int64_t d, int n_h
     if (!ws || ws_bytes < span_bytes(N, o.n_seq)) return TP_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return TP_ERR_ALIGN;
   }
+  return fwd_works(N, n_heads, sh) > INT_MAX ? TP_ERR_SHAPE : TP_OK;
+}
+
+tp_status run_window_attn_fwd(const uint16_t* QKV, int64_t N, int64_t d, int n_heads, int n_kv, int head_dim, int t,
+                              const WindowAttn& o, float scale, uint16_t* O, float* lse, int zero_pad, void* ws,
+                              size_t ws_bytes, cudaStream_t s) {
+  TP_RETURN_IF(window_attn_fwd_ok(QKV, N, d, n_heads, n_kv, head_dim, t, o, O, lse, ws, ws_bytes));
+  if (N == 0) return TP_OK;
+  AttnShape sh;
+  TP_RETURN_IF(check_window(N, d, n_heads, n_kv, head_dim, t, o, sh));
   WinArgs a{};
   fill_args(a, N, n_heads, t, o, sh, scale);
-  const int64_t grid = a.by_head ? static_cast<int64_t>(n_heads / 2) * a.nqb
-                                 : static_cast<int64_t>(n_heads) * ((a.nqb + 1) / 2);
-  if (grid > INT_MAX) return TP_ERR_SHAPE;
+  const int64_t grid = fwd_works(N, n_heads, sh);
   TP_RETURN_IF(ready());
   a.err = device_error_word();
   a.QKV = QKV;
@@ -1995,9 +2015,9 @@ size_t window_attn_bwd_ws_bytes(int64_t N, int64_t d, int n_heads, int n_kv, int
   return span_bytes(N, n_seq) + far_plan(N, t * sh.kv_t, r.W, r.S, n_seq).bytes;
 }
 
-tp_status run_window_attn_bwd(const uint16_t* QKV, const uint16_t* O, const uint16_t* dO, const float* lse, int64_t N,
-                              int64_t d, int n_heads, int n_kv, int head_dim, int t, const WindowAttn& o, float scale,
-                              float* Dvec, uint16_t* dQKV, int dqkv_f16, void* ws, size_t ws_bytes, cudaStream_t s) {
+tp_status window_attn_bwd_ok(const uint16_t* QKV, const uint16_t* O, const uint16_t* dO, const float* lse, int64_t N,
+                             int64_t d, int n_heads, int n_kv, int head_dim, int t, const WindowAttn& o,
+                             const float* Dvec, const uint16_t* dQKV, const void* ws, size_t ws_bytes) {
   AttnShape sh;
   TP_RETURN_IF(check_window(N, d, n_heads, n_kv, head_dim, t, o, sh));
   if (N == 0) return TP_OK;
@@ -2014,12 +2034,22 @@ tp_status run_window_attn_bwd(const uint16_t* QKV, const uint16_t* O, const uint
   const size_t need = window_attn_bwd_ws_bytes(N, d, n_heads, n_kv, head_dim, t, o.window, o.n_sink, o.n_seq);
   if (need > 0 && (!ws || ws_bytes < need)) return TP_ERR_WORKSPACE;
   if (need > 0 && (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return TP_ERR_ALIGN;
+  const Reach r = reach_of(N, o.window, o.n_sink);
+  const BwdWorks w = bwd_works(N, n_heads, t * sh.kv_t, far_plan(N, t * sh.kv_t, r.W, r.S, o.n_seq));
+  return w.q > INT_MAX || w.far + w.kv > INT_MAX ? TP_ERR_SHAPE : TP_OK;
+}
+
+tp_status run_window_attn_bwd(const uint16_t* QKV, const uint16_t* O, const uint16_t* dO, const float* lse, int64_t N,
+                              int64_t d, int n_heads, int n_kv, int head_dim, int t, const WindowAttn& o, float scale,
+                              float* Dvec, uint16_t* dQKV, int dqkv_f16, void* ws, size_t ws_bytes, cudaStream_t s) {
+  TP_RETURN_IF(window_attn_bwd_ok(QKV, O, dO, lse, N, d, n_heads, n_kv, head_dim, t, o, Dvec, dQKV, ws, ws_bytes));
+  if (N == 0) return TP_OK;
+  AttnShape sh;
+  TP_RETURN_IF(check_window(N, d, n_heads, n_kv, head_dim, t, o, sh));
   WinArgs a{};
   fill_args(a, N, n_heads, t, o, sh, scale);
   const FarPlan f = far_plan(N, a.Hkv, a.W, a.S, o.n_seq);
-  const int64_t grid_q = static_cast<int64_t>(n_heads) * a.nqb, grid_kv = static_cast<int64_t>(a.Hkv) * a.nqb;
-  const int64_t grid_far = static_cast<int64_t>(a.Hkv) * f.nch * f.nsb;
-  if (grid_q > INT_MAX || grid_far + grid_kv > INT_MAX) return TP_ERR_SHAPE;
+  const BwdWorks works = bwd_works(N, n_heads, a.Hkv, f);
   TP_RETURN_IF(ready());
   a.err = device_error_word();
   a.QKV = QKV;
@@ -2033,7 +2063,7 @@ tp_status run_window_attn_bwd(const uint16_t* QKV, const uint16_t* O, const uint
   a.C = f.C;
   a.nch = f.nch;
   a.nsb = f.nsb;
-  a.nfar = static_cast<int>(grid_far);
+  a.nfar = static_cast<int>(works.far);
   a.far = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + span_bytes(N, o.n_seq));
   CUtensorMap m_qkv, m_do;
   if (!make_map_3d_bf16(&m_qkv, QKV, sh.row_w, N, t, sh.row_w * 2, N * sh.row_w * 2, 64, 64) ||
@@ -2050,19 +2080,19 @@ tp_status run_window_attn_bwd(const uint16_t* QKV, const uint16_t* O, const uint
   }
   int* total = o.n_seq > 0 ? static_cast<int*>(ws) : nullptr;
   int2* span = o.n_seq > 0 ? reinterpret_cast<int2*>(static_cast<uint8_t*>(ws) + 256) : nullptr;
-  TP_CUDA_CHECK(launch_pdl(window_prep_kernel, dim3(static_cast<unsigned>(grid_kv)), dim3(PREP_THREADS), 0, s, a,
+  TP_CUDA_CHECK(launch_pdl(window_prep_kernel, dim3(static_cast<unsigned>(works.kv)), dim3(PREP_THREADS), 0, s, a,
                            o.cu_seqlens, static_cast<int>(o.n_seq), total, span));
   count_launch();
   a.total = total;
   a.span = span;
-  TP_CUDA_CHECK(launch_pdl(window_dq_kernel, dim3(static_cast<unsigned>(grid_q)), dim3(DQ_THREADS), DQ_SMEM, s, m_qkv,
+  TP_CUDA_CHECK(launch_pdl(window_dq_kernel, dim3(static_cast<unsigned>(works.q)), dim3(DQ_THREADS), DQ_SMEM, s, m_qkv,
                            m_do, a));
   count_launch();
-  TP_CUDA_CHECK(launch_pdl(window_dkv_kernel, dim3(static_cast<unsigned>(grid_far + grid_kv)), dim3(BWD_THREADS), DKV_SMEM,
+  TP_CUDA_CHECK(launch_pdl(window_dkv_kernel, dim3(static_cast<unsigned>(works.far + works.kv)), dim3(BWD_THREADS), DKV_SMEM,
                            s, m_qkv, m_do, a));
   count_launch();
-  if (grid_far > 0) {
-    TP_CUDA_CHECK(launch_pdl(window_sink_kernel, dim3(static_cast<unsigned>(grid_kv)), dim3(SINK_THREADS), 0, s, a));
+  if (works.far > 0) {
+    TP_CUDA_CHECK(launch_pdl(window_sink_kernel, dim3(static_cast<unsigned>(works.kv)), dim3(SINK_THREADS), 0, s, a));
     count_launch();
   }
   return TP_OK;

@@ -276,3 +276,32 @@ def test_blocks_check_the_buffers_of_out():
     with pytest.raises(ValueError, match="ws is on"):
         T.window_decode_attn(torch.zeros(3, 4, 128, dtype=torch.float16), cache, cache.clone(),
                              torch.zeros(3, dtype=torch.int32), 2, 4, ws=ws)
+
+
+def test_blocks_refuse_before_they_launch():
+    """What a block's later steps refuse is refused before its first: here a launch would give TP_ERR_CUDA."""
+    ok = dict(window=8, n_sink=2, inv_freq=P, rot_dim=64)
+    need = L.tp_decode_attn_opt_workspace_size(2, 512, 4, 2, 128, 1)
+
+    def dec(x=P, k=2 * P, v=4 * P, pos=8 * P, y=16 * P, ws=32 * P, o=None):
+        return L.tp_decode_attn_opt_forward(x, 2, 512, 4, 2, 128, 1, 0.1, o or opts(**ok), P, None, P, None, k, v, 64, pos, y,
+                                            ws, need, **C)
+    cache = 2 * 2 * 64 * 128 * 2
+    assert dec(k=4 * P) == dec(v=2 * P + cache - 256) == L.TP_ERR_INVALID_ARG          # the caches over each other
+    assert dec(k=32 * P) == dec(v=32 * P - cache + 256) == L.TP_ERR_INVALID_ARG        # over the workspace
+    assert dec(pos=8 * P + 2) == L.TP_ERR_ALIGN
+
+    def fwd_(raw=None, q=2 * P, O=4 * P, lse=8 * P, N=40, ws=None, nws=0, **o):
+        return L.tp_attn_opt_forward(P, N, 512, 4, 2, 128, 1, 0.1, opts(**{**ok, **o}), P, None, P, None, None, 16 * P, raw, q,
+                                     O, lse, 0, ws, nws, **C)
+    assert fwd_(raw=2 * P + 16) == fwd_(raw=2 * P - 1024) == L.TP_ERR_INVALID_ARG       # the raw rows partly over the rotated
+    assert fwd_(O=2 * P + 1024) == fwd_(lse=2 * P + 64) == fwd_(lse=4 * P + 64) == L.TP_ERR_INVALID_ARG
+    assert fwd_(N=(1 << 29) + 1) == L.TP_ERR_SHAPE
+
+    def bwd(raw=64 * P, qkv=2 * P, O=4 * P, lse=8 * P, ws=32 * P, N=40):
+        o = opts(**ok, q_gamma=P, k_gamma=P, eps=1e-6)
+        return L.tp_attn_opt_backward(16 * P, P, raw, qkv, O, lse, N, 512, 4, 2, 128, 1, 0.1, o, P, P, 128 * P, 256 * P, None,
+                                      256 * P, None, None, None, 0, 0, ws, 1 << 62, **C)
+    inside = 32 * P + 4096
+    assert bwd(qkv=inside) == bwd(O=inside) == bwd(lse=inside) == bwd(raw=inside) == L.TP_ERR_INVALID_ARG
+    assert bwd(N=(1 << 29) + 1) == L.TP_ERR_SHAPE
