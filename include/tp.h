@@ -566,7 +566,8 @@ tp_status tp_attn_window_backward(const uint16_t* QKV, const tp_bf16* O, const u
  * tp_get_device_status() report TP_ERR_SHAPE.  window >= 1, n_sink >= 0; head_dim == 128, t
  * <= 8, query heads per KV group on one shard <= 32; cache tiles of 128 keys, over all
  * streams, below 2^24.  ws: tp_window_decode_workspace_size() bytes, 256-byte aligned (the
- * fp32 partials of split sequences).  Two launches. */
+ * fp32 partials of split sequences).  O and ws must not overlap Q, the caches, pos or each
+ * other (TP_ERR_INVALID_ARG).  Two launches. */
 size_t tp_window_decode_workspace_size(int64_t B, int n_heads, int n_kv_heads, int head_dim, int t);
 tp_status tp_window_decode_forward(const uint16_t* Q, int64_t B, int n_heads, int n_kv_heads, int head_dim, int t,
                                    int64_t window, int64_t n_sink, int rolling, float scale, const uint16_t* K_cache,
@@ -625,7 +626,8 @@ tp_status tp_attn_opt_backward(const tp_bf16* dY, const tp_bf16* X, const uint16
  * unspecified).  The projected rows are rounded to IEEE fp16 before the norm and rotation, as
  * the forward's are (a value above 65504 becomes infinite).  The caches hold rotated keys;
  * slots as tp_qk_norm_rope_append.  ws:
- * tp_decode_attn_opt_workspace_size() bytes, 256-byte aligned. */
+ * tp_decode_attn_opt_workspace_size() bytes, 256-byte aligned, over none of the other
+ * arguments; y not over a cache (TP_ERR_INVALID_ARG). */
 size_t tp_decode_attn_opt_workspace_size(int64_t B, int64_t d, int n_heads, int n_kv_heads, int head_dim, int t);
 tp_status tp_decode_attn_opt_forward(const tp_bf16* x, int64_t B, int64_t d, int n_heads, int n_kv_heads, int head_dim,
                                      int t, float scale, const tp_attn_options* opt, const tp_bf16* Wqkv_p,

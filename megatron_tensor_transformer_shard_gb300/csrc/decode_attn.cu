@@ -1052,7 +1052,15 @@ tp_status window_decode_ok(const uint16_t* Q, int64_t B, int n_heads, int n_kv, 
   if (!aligned16(Q) || !aligned16(Kc) || !aligned16(Vc) || !aligned16(O) || (reinterpret_cast<uintptr_t>(pos) & 3u) != 0 ||
       (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
     return TP_ERR_ALIGN;
-  if (!ws || ws_bytes < window_ws_layout(nullptr, sh).bytes) return TP_ERR_WORKSPACE;
+  const size_t need = window_ws_layout(nullptr, sh).bytes;
+  if (!ws || ws_bytes < need) return TP_ERR_WORKSPACE;
+  const size_t qb = static_cast<size_t>(B) * n_heads * HD * 2, cache = static_cast<size_t>(sh.S) * L_max * HD * 2;
+  const size_t pb = static_cast<size_t>(B) * 4;
+  auto meets_input = [&](const void* p, size_t bytes) {
+    return overlap(p, bytes, Q, qb) || overlap(p, bytes, Kc, cache) || overlap(p, bytes, Vc, cache) ||
+           overlap(p, bytes, pos, pb);
+  };
+  if (meets_input(O, qb) || meets_input(ws, need) || overlap(O, qb, ws, need)) return TP_ERR_INVALID_ARG;
   return TP_OK;
 }
 
@@ -1170,6 +1178,10 @@ tp_status run_decode_opt(const uint16_t* x, int64_t B, int64_t d, int n_heads, i
                                       rolling, 1));
   TP_RETURN_IF(window_decode_ok(w.q, B, n_heads, n_kv, head_dim, t, window, n_sink, rolling, Kc, Vc, L_max, pos, w.O,
                                 w.core, w.core_bytes));
+  const size_t cache = static_cast<size_t>(sh.S) * L_max * HD * 2, xb = static_cast<size_t>(B) * d * 2;
+  if (overlap(ws, w.bytes, Kc, cache) || overlap(ws, w.bytes, Vc, cache) || overlap(ws, w.bytes, x, xb) ||
+      overlap(ws, w.bytes, y, xb) || overlap(y, xb, Kc, cache) || overlap(y, xb, Vc, cache))
+    return TP_ERR_INVALID_ARG;
   TP_RETURN_IF(ready());
   const int64_t nq = static_cast<int64_t>(n_heads) * HD;
   // The rows before norm and rotation are fp16, as the caches and the prompt's block hold them: a token that is

@@ -305,3 +305,23 @@ def test_blocks_refuse_before_they_launch():
     inside = 32 * P + 4096
     assert bwd(qkv=inside) == bwd(O=inside) == bwd(lse=inside) == bwd(raw=inside) == L.TP_ERR_INVALID_ARG
     assert bwd(N=(1 << 29) + 1) == L.TP_ERR_SHAPE
+
+
+def test_window_decode_refuses_overlaps():
+    need = L.tp_window_decode_workspace_size(2, 4, 2, 128, 1)
+    qb, cache = 2 * 4 * 128 * 2, 2 * 2 * 64 * 128 * 2
+
+    def dec(q=P, k=2 * P, v=4 * P, pos=8 * P, o=16 * P, ws=32 * P):
+        return L.tp_window_decode_forward(q, 2, 4, 2, 128, 1, 8, 0, 0, 0.1, k, v, 64, pos, o, ws, need, **C)
+    assert dec(o=P) == dec(o=P + qb - 16) == dec(o=P - qb + 16) == L.TP_ERR_INVALID_ARG                # the queries
+    assert dec(o=2 * P + cache - 16) == dec(o=4 * P) == dec(o=8 * P) == L.TP_ERR_INVALID_ARG           # caches, positions
+    assert dec(o=32 * P + 256) == dec(o=32 * P - 256) == L.TP_ERR_INVALID_ARG                          # the workspace
+    assert dec(q=32 * P + 256) == dec(k=32 * P) == dec(v=32 * P - 256) == dec(pos=32 * P + need - 4) == L.TP_ERR_INVALID_ARG
+    ok = dict(window=8, n_sink=2)
+    total = L.tp_decode_attn_opt_workspace_size(2, 512, 4, 2, 128, 1)
+
+    def step(x=P, k=2 * P, v=4 * P, y=16 * P, ws=32 * P):
+        return L.tp_decode_attn_opt_forward(x, 2, 512, 4, 2, 128, 1, 0.1, opts(**ok), P, None, P, None, k, v, 64, 8 * P, y, ws,
+                                            total, **C)
+    assert step(y=2 * P) == step(y=4 * P + cache - 16) == step(y=32 * P + total - 16) == L.TP_ERR_INVALID_ARG
+    assert step(x=32 * P + total - 16) == step(k=32 * P + total - 256) == L.TP_ERR_INVALID_ARG
