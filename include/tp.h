@@ -448,7 +448,8 @@ tp_status tp_attn_gqa_backward(const tp_bf16* dY, const tp_bf16* X, const uint16
  *   QKV IEEE fp16, or bf16 with TP_QKNR_BF16_INPUT (what tp_column_parallel_forward
  *   writes); QKV_out IEEE fp16 (tp_attn_core_forward's operand type).  QKV_out == QKV
  *   works in place; other overlaps are refused (TP_ERR_INVALID_ARG).
- *   q_gamma, k_gamma [128] bf16: both, or both NULL for no norm; eps >= 0.
+ *   q_gamma, k_gamma [128] bf16: both, or both NULL for no norm; eps >= 0 (with eps = 0 a head
+ *   of zeros stays zeros, with a zero gradient).
  *   inv_freq: DEVICE double [rot_dim / 2], f_i in radians per position, NULL for no
  *   rotation (not together with no norm); rot_dim a multiple of 16, 16..128.  The phase
  *   p f_i is formed modulo a turn in 64-bit integers: exact for every int32 position.

@@ -194,28 +194,32 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// r = 1 / rms of a head.  A sum of squares that overflows fp32 (|x| above 10^18) is formed again
-// from values scaled by 2^-64, and x is left scaled with r to match, so that every finite bf16
-// row gets its finite result (eps is far below such a row's mean square); r_true is 1 / rms.
+// r = 1 / rms of a head.  A sum of squares that leaves fp32 at the top (|x| above 10^18), or one that
+// loses bits at the bottom with an eps no larger (below 2^-100 together), is formed again from values
+// scaled by 2^-64 or 2^64, and x is left scaled with r to match, so that every finite bf16 row gets its
+// result (at the top eps is far below such a row's mean square); r_true is 1 / rms.  Zeros with eps = 0
+// have r = 0: they stay zeros and get no gradient.
 __device__ __forceinline__ float inv_rms(Pairs& x, float eps, float& r_true) {
   auto squares = [&]() {
     return f2_fma(x.a[0], x.a[0], f2_fma(x.a[1], x.a[1], f2_fma(x.b[0], x.b[0], f2_mul(x.b[1], x.b[1]))));
   };
   const float ss = group_sum(f2_sum(squares()));
-  float r = r_true = rsqrtf(fmaf(ss, 1.0f / HD, eps));
-  const bool over = ss > 3.0e38f;
-  if (__any_sync(0xffffffffu, over)) {
-    const float d = over ? 5.42101086e-20f : 1.0f;
-    const uint64_t down = f2_pack(d, d);
+  const float ms = fmaf(ss, 1.0f / HD, eps);
+  float r = r_true = rsqrtf(ms);
+  const bool over = ss > 3.0e38f, under = ms < 7.9e-31f;
+  if (__any_sync(0xffffffffu, over || under)) {
+    const float d = over ? 5.42101086e-20f : under ? 18446744073709551616.0f : 1.0f;  // 2^-64, 2^64
+    const uint64_t scaled = f2_pack(d, d);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      x.a[k] = f2_mul(x.a[k], down);
-      x.b[k] = f2_mul(x.b[k], down);
+      x.a[k] = f2_mul(x.a[k], scaled);
+      x.b[k] = f2_mul(x.b[k], scaled);
     }
     const float s2 = group_sum(f2_sum(squares()));
-    if (over) {
-      r = rsqrtf(s2 * (1.0f / HD));
-      r_true = r * 5.42101086e-20f;
+    if (over || under) {
+      const float m2 = over ? s2 * (1.0f / HD) : fmaf(s2, 1.0f / HD, eps * d * d);
+      r = m2 > 0.0f ? rsqrtf(m2) : 0.0f;
+      r_true = fminf(r * d, 3.4e38f);  // finite, as it may meet a 0
     }
   }
   return r;
@@ -517,9 +521,7 @@ __global__ void __launch_bounds__(STREAM_THREADS, 1) qk_norm_rope_stream_kernel(
             Pairs x = to_pairs<ROT, BF16>(on ? cols.load(xslot + (h + grp - h0) * HD) : make_uint4(0u, 0u, 0u, 0u));
             float r_true;
             const float r = inv_rms(x, a.eps, r_true);
-            // a head behind the last is 0; with eps = 0 its r is infinite, and 0 * r would not be 0
-            const float ra = on ? r : 0.0f;
-            const uint64_t r2 = f2_pack(ra, ra), out2 = f2_pack(r_true, r_true);
+            const uint64_t r2 = f2_pack(r, r), out2 = f2_pack(r_true, r_true);
             uint64_t dot2 = 0;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {

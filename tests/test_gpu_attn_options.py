@@ -208,3 +208,27 @@ def test_decode_holds_its_rows_in_fp16(B):
         off = (off + np.abs(rows[:, part]) * (off ** 2).mean(1, keepdims=True) ** 0.5 /
                np.sqrt((rows[:, part] ** 2).mean(1, keepdims=True))) * gain
         assert (np.abs(f64(K[i, 0, :, 0]) - key[0][:, part]) <= tol[0][:, part] + off).all()
+
+
+def test_padding_of_zeros_leaves_the_gradients_alone():
+    """Rows of no sequence that are zeros, no bias, eps = 0: their norm has nothing to divide by, and the parameters'
+    gradients are those of the sequences alone."""
+    n_heads, n_kv, t, N, n = 4, 2, 2, 200, 130
+    inp = I.gqa_attn_inputs(N, 512, n_heads, n_kv, 128, bias=False, seed=3)
+    dev = {k: v.cuda() for k, v in inp.items() if v is not None}
+    w = T.DecodeAttnWeights(dev["W_qkv"], None, dev["W_o"], None, n_heads, n_kv, 128, t)
+    g = torch.ones(128, dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, 60, n], dtype=torch.int32, device="cuda")
+    X, dY = dev["X"].clone(), dev["dY"].clone()
+    X[n:], dY[n:] = 0, 0
+
+    def grads(X, dY, cu):
+        opt = T.AttentionOptions(50, 2, g, g, 0.0, T.rope_frequencies(128), cu_seqlens=cu)
+        out = T.attn_opt_forward(X, w.Wqkv_p, None, w.Wo_p, None, n_heads, n_kv, t, opt)
+        return T.attn_opt_backward(dY, X, *out[1:], w.Wqkv_p, w.Wo_p, n_heads, n_kv, t, opt)
+    a, b = grads(X, dY, cu), grads(X[:n].contiguous(), dY[:n].contiguous(), cu)
+    assert not a["dX"][n:].any()
+    for k in ("q_gamma", "k_gamma", "Wqkv_p", "Wo_p"):
+        assert torch.isfinite(a[k]).all()
+        assert_close(k, f64(a[k]), f64(b[k]), 1e-5)
+    assert_close("dX", f64(a["dX"][:n]), f64(b["dX"]))

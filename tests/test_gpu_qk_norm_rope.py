@@ -290,3 +290,71 @@ def test_rows_past_32_bit_offsets():
         m = n * (h.stop - h.start)
         assert ((a - b).abs() <= 2 * m * 2.0 ** -24 * terms[:, h].sum((0, 1))).all()
     assert L.tp_get_device_status(check=False) == L.TP_OK
+
+
+def gamma_units(t, N, n_heads, n_kv):
+    """Roundings in the longest chain of a gamma gradient, in halves of fp32's last place.  12 warps an SM share out
+    the units, runs of up to 10 heads of a row (fewer when there are few rows); a 16-lane group adds up every second
+    head of its units, then come 24 groups, every 64th CTA, 6 levels; and 56 for each term itself (24 as in the
+    forward, the products, 16 of the phase)."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    per = n_heads // t + 2 * max(1, n_kv // t)
+    chunks = max(-(-per // 10), min(per, -(-sms * 12 // (t * N))))
+    heads = -(-per // chunks)
+    chunks = -(-per // heads)
+    visits = -(-t * N * chunks // (min(sms, t * N * chunks) * 12)) * -(-heads // 2)
+    return (visits + 24 + -(-sms // 64) + 6 + 56) * 2.0 ** -24
+
+
+def test_rows_of_any_magnitude_without_eps():
+    """eps = 0: small rows, whose squares leave fp32 at the bottom, are normed like any other; zeros stay zeros, have
+    no gradient and leave the gamma gradients alone."""
+    n_heads, n_kv, t, N = 4, 2, 2, 12
+    X = rnd(1, t, N, width(n_heads, n_kv, t), dtype=torch.bfloat16)
+    G = rnd(5, *X.shape, dtype=torch.bfloat16)
+    for row, e in ((1, -40), (2, -60), (3, -80), (4, -110), (5, -125), (6, 60)):
+        X[:, row] *= 2.0 ** e
+        G[:, row] *= 2.0 ** e                       # a gradient that leaves the result in bf16's range
+    X[:, 7] = 0
+    X[0, 8, 128:256] = 0                            # one head of a row
+    X[:, :, 384:] = 1.0                             # the carried values
+    gq, gk = gammas(2, True)
+    f = T.rope_frequencies(128, 500000.0, "cpu")
+    zero = np.zeros(X.shape, bool)
+    zero[:, 7, :384] = zero[0, 8, 128:256] = True
+    stand_in = f64(X)
+    stand_in[zero] = 1.0                            # the oracle divides by 0 there
+    ref, tol = O.qk_norm_rope(stand_in, n_heads, n_kv, f64(gq), f64(gk), 0.0, f.numpy())
+    Xd, Gd, gqd, gkd, fd = cuda(X, G, gq, gk, f)
+    Y = T.qk_norm_rope_forward(Xd, n_heads, n_kv, gqd, gkd, 0.0, fd)
+    ref[zero] = 0
+    within(Y, ref, tol)
+    assert not Y.cpu().numpy()[zero].any()
+    Gz = f64(G)
+    Gz[zero] = 0                                    # no gradient through zeros
+    dX, dq, dk, bX, bq, bk = O.qk_norm_rope_backward(Gz, stand_in, n_heads, n_kv, f64(gq), f64(gk), 0.0, f.numpy())
+    # a rotated pair never mixes heads, so a zero head's gradient reaches nothing else
+    got = T.qk_norm_rope_backward(Gd, Xd, n_heads, n_kv, gqd, gkd, 0.0, fd)
+    dX[zero] = 0
+    within(got[0], dX, 2.0 ** -8 * np.abs(dX) + 84 * 2.0 ** -24 * bX)
+    units = gamma_units(t, N, n_heads, n_kv)
+    within(got[1], dq, units * bq)
+    within(got[2], dk, units * bk)
+    K, V = (torch.zeros(t, 1, N, 16, 128, dtype=torch.float16, device="cuda") for _ in range(2))
+    pos = torch.arange(N, dtype=torch.int32, device="cuda")
+    Q = T.qk_norm_rope_append(Xd, n_heads, n_kv, K, V, pos, gqd, gkd, 0.0, fd)
+    assert torch.equal(Q.view(N, t, 256).transpose(0, 1), Y[:, :, :256])
+    assert torch.equal(K[:, 0, torch.arange(N), torch.arange(N)], Y[:, :, 256:384])
+
+
+@pytest.mark.parametrize("n_heads,n_kv,t,N", [(64, 8, 4, 3001), (12, 4, 1, 20000), (8, 8, 2, 37)])
+def test_gamma_gradients_within_the_longest_chain(n_heads, n_kv, t, N):
+    X = rnd(1, t, N, width(n_heads, n_kv, t))
+    G = rnd(2, *X.shape, dtype=torch.bfloat16)
+    gq, gk = gammas(3, True)
+    f = T.rope_frequencies(128, device="cpu")
+    _, dq, dk, _, bq, bk = O.qk_norm_rope_backward(f64(G), f64(X), n_heads, n_kv, f64(gq), f64(gk), 1e-6, f.numpy())
+    got = T.qk_norm_rope_backward(*cuda(G, X), n_heads, n_kv, *cuda(gq, gk), inv_freq=f.cuda())
+    units = gamma_units(t, N, n_heads, n_kv)
+    within(got[1], dq, units * bq)
+    within(got[2], dk, units * bk)
