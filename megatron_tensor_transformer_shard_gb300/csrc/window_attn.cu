@@ -108,10 +108,12 @@ struct WinArgs {
   uint64_t timeout_ns;
 };
 
-__device__ __forceinline__ int total_rows(const WinArgs& p) { return p.total ? __ldg(p.total) : p.N; }
+// Plain loads, as for all that an earlier kernel writes: this one may have started before it was done, so its data is
+// not read-only for the whole kernel, as a non-coherent load would need.
+__device__ __forceinline__ int total_rows(const WinArgs& p) { return p.total ? *p.total : p.N; }
 __device__ __forceinline__ int2 span_of(const WinArgs& p, int row) {
   if (row >= p.N) return make_int2(row, row);
-  return p.span ? __ldg(p.span + row) : make_int2(0, p.N);
+  return p.span ? p.span[row] : make_int2(0, p.N);
 }
 
 // Key blocks (of 2^LOG keys) that the 128 queries from q0 see: [a0, a1) hold sinks behind the
@@ -1614,8 +1616,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           const int64_t off = at + min(r0 + 2 * u + half, rows - 1) * p.dt;
-          o[u] = __ldg(reinterpret_cast<const uint4*>(p.O + off));
-          g[u] = __ldg(reinterpret_cast<const uint4*>(p.dO + off));
+          o[u] = *reinterpret_cast<const uint4*>(p.O + off);
+          g[u] = *reinterpret_cast<const uint4*>(p.dO + off);
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
