@@ -1049,7 +1049,7 @@ tp_status window_decode_ok(const uint16_t* Q, int64_t B, int n_heads, int n_kv, 
   if (static_cast<int64_t>(sh.S) * ((L_max + BK - 1) / BK + 1) >= (1LL << 24)) return TP_ERR_SHAPE;
   if (B == 0) return TP_OK;
   if (!Q || !Kc || !Vc || !pos || !O) return TP_ERR_INVALID_ARG;
-  if (!aligned16(Q) || !aligned16(Kc) || !aligned16(Vc) || !aligned16(O) || (reinterpret_cast<uintptr_t>(pos) & 3u) != 0 ||
+  if (!aligned16(Q) || !aligned16(Kc) || !aligned16(Vc) || !aligned16(O) || !aligned4(pos) ||
       (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
     return TP_ERR_ALIGN;
   const size_t need = window_ws_layout(nullptr, sh).bytes;

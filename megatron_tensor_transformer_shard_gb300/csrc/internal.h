@@ -25,6 +25,7 @@ inline bool overlap(const void* p, size_t n, const void* q, size_t m) {
   return x < y + m && y < x + n;
 }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 #define TP_RETURN_IF(expr)        \
   do {                            \

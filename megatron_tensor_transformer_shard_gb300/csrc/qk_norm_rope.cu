@@ -730,7 +730,7 @@ tp_status check_common(const QkNormRope& o, int64_t N, int n_heads, int n_kv, in
   }
   if (N > (1LL << 30)) return TP_ERR_SHAPE;
   if (!aligned16(o.q_gamma) || !aligned16(o.k_gamma) || (reinterpret_cast<uintptr_t>(o.inv_freq) & 7u) != 0 ||
-      (reinterpret_cast<uintptr_t>(o.pos) & 3u) != 0)
+      !aligned4(o.pos))
     return TP_ERR_ALIGN;
   a.N = N;
   a.rows = N * t;
@@ -789,6 +789,7 @@ tp_status check_bwd(const uint16_t* dQKV, const uint16_t* QKV, int64_t N, int n_
                     size_t ws_bytes, QkArgs& a, int& rot, bool& norm) {
   TP_RETURN_IF(check_common(o, N, n_heads, n_kv, head_dim, t, a, rot, norm));
   if (!norm && (dq_gamma || dk_gamma)) return TP_ERR_INVALID_ARG;
+  if (!aligned4(dq_gamma) || !aligned4(dk_gamma)) return TP_ERR_ALIGN;
   if (N == 0) return TP_OK;
   if (!dQKV || !out || (norm && !QKV)) return TP_ERR_INVALID_ARG;
   if (!aligned16(dQKV) || !aligned16(QKV) || !aligned16(out)) return TP_ERR_ALIGN;

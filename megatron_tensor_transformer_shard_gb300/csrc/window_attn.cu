@@ -1899,7 +1899,7 @@ tp_status check_window(int64_t N, int64_t d, int n_heads, int n_kv, int head_dim
   if (!attn_shape(d, n_heads, n_kv, head_dim, t, sh)) return TP_ERR_SHAPE;
   // row indices and their sums with the window fit 32 bits (2^29 rows of QKV have 400 GB)
   if (N > (1LL << 29) || o.n_seq > (1LL << 30)) return TP_ERR_SHAPE;
-  if ((reinterpret_cast<uintptr_t>(o.cu_seqlens) & 3u) != 0) return TP_ERR_ALIGN;
+  if (!aligned4(o.cu_seqlens)) return TP_ERR_ALIGN;
   return TP_OK;
 }
 
@@ -1960,7 +1960,7 @@ tp_status window_attn_fwd_ok(const uint16_t* QKV, int64_t N, int64_t d, int n_he
   TP_RETURN_IF(check_window(N, d, n_heads, n_kv, head_dim, t, o, sh));
   if (N == 0) return TP_OK;
   if (!QKV || !O || !lse) return TP_ERR_INVALID_ARG;
-  if (!aligned16(QKV) || !aligned16(O)) return TP_ERR_ALIGN;
+  if (!aligned16(QKV) || !aligned16(O) || !aligned4(lse)) return TP_ERR_ALIGN;
   const size_t qkv_bytes = static_cast<size_t>(t) * N * sh.row_w * 2, o_bytes = static_cast<size_t>(t) * N * sh.dt * 2;
   const size_t lse_bytes = static_cast<size_t>(n_heads) * N * 4;
   if (overlap(QKV, qkv_bytes, O, o_bytes) || overlap(QKV, qkv_bytes, lse, lse_bytes) ||
@@ -2024,7 +2024,8 @@ tp_status window_attn_bwd_ok(const uint16_t* QKV, const uint16_t* O, const uint1
   TP_RETURN_IF(check_window(N, d, n_heads, n_kv, head_dim, t, o, sh));
   if (N == 0) return TP_OK;
   if (!QKV || !O || !dO || !lse || !Dvec || !dQKV) return TP_ERR_INVALID_ARG;
-  if (!aligned16(QKV) || !aligned16(O) || !aligned16(dO) || !aligned16(dQKV)) return TP_ERR_ALIGN;
+  if (!aligned16(QKV) || !aligned16(O) || !aligned16(dO) || !aligned16(dQKV) || !aligned4(lse) || !aligned4(Dvec))
+    return TP_ERR_ALIGN;
   const size_t qkv_bytes = static_cast<size_t>(t) * N * sh.row_w * 2, o_bytes = static_cast<size_t>(t) * N * sh.dt * 2;
   const size_t lse_bytes = static_cast<size_t>(n_heads) * N * 4;
   auto meets_input = [&](const void* p, size_t bytes) {

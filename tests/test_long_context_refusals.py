@@ -325,3 +325,17 @@ def test_window_decode_refuses_overlaps():
                                             total, **C)
     assert step(y=2 * P) == step(y=4 * P + cache - 16) == step(y=32 * P + total - 16) == L.TP_ERR_INVALID_ARG
     assert step(x=32 * P + total - 16) == step(k=32 * P + total - 256) == L.TP_ERR_INVALID_ARG
+
+
+def test_fp32_pointers_between_words_are_refused():
+    assert wfwd(lse=4 * P + 2) == L.TP_ERR_ALIGN
+
+    def wbwd(lse=32 * P, D=16 * P):
+        return L.tp_attn_window_backward(P, 4 * P, 8 * P, lse, 4, 512, 4, 2, 128, 1, 8, 0, 0.1, None, 0, D, 2 * P, 0, None, 0,
+                                         **C)
+    assert wbwd(lse=32 * P + 2) == wbwd(D=16 * P + 1) == L.TP_ERR_ALIGN
+
+    def nbwd(N=4, dq=P, dk=P):
+        return L.tp_qk_norm_rope_backward(P, 2 * P, N, 4, 2, 128, 1, P, P, 1e-6, P, 128, None, 4 * P, dq, dk, 0, 0, P,
+                                          L.tp_qk_norm_rope_backward_workspace_size(), **C)
+    assert nbwd(dq=P + 2) == nbwd(dk=P + 1) == nbwd(N=0, dq=P + 2) == L.TP_ERR_ALIGN
