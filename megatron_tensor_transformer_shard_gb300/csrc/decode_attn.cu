@@ -249,6 +249,27 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
   int* pre = reinterpret_cast<int*>(base + C::OFF_PRE);     // [B + 1] tile prefix of the sequences
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      ptx::mbar_init(&k_full[s], 1);
+      ptx::mbar_init(&v_full[s], 1);
+      ptx::mbar_init(&k_empty[s], 1);
+      ptx::mbar_init(&v_empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&q_full[b], 1);
+      ptx::mbar_init(&q_empty[b], 1);
+      ptx::mbar_init(&s_full[b], 1);
+      ptx::mbar_init(&s_free[b], 128);
+      ptx::mbar_init(&p_full[b], 128);
+      ptx::mbar_init(&o_full[b], 1);
+      ptx::mbar_init(&o_free[b], 128);
+    }
+    ptx::mbar_init(mma_done, 1);
+    ptx::mbar_init(all_done, DEC_THREADS);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
   // WIN: this is the first kernel of the call, and the one before it on the stream may write pos, so
   // every thread waits for it before anything is read; then CTAs without a tile, which return below,
   // are behind that kernel too, and so is whoever waits for this grid.  Otherwise the projection's last
@@ -271,27 +292,6 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
   const int x1 = static_cast<int>((static_cast<int64_t>(k + 1) * T) / G);
   if (x0 >= x1) return;  // uniform for the whole CTA, before any barrier or TMEM use
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < ST; ++s) {
-      ptx::mbar_init(&k_full[s], 1);
-      ptx::mbar_init(&v_full[s], 1);
-      ptx::mbar_init(&k_empty[s], 1);
-      ptx::mbar_init(&v_empty[s], 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      ptx::mbar_init(&q_full[b], 1);
-      ptx::mbar_init(&q_empty[b], 1);
-      ptx::mbar_init(&s_full[b], 1);
-      ptx::mbar_init(&s_free[b], 128);
-      ptx::mbar_init(&p_full[b], 128);
-      ptx::mbar_init(&o_full[b], 1);
-      ptx::mbar_init(&o_free[b], 128);
-    }
-    ptx::mbar_init(mma_done, 1);
-    ptx::mbar_init(all_done, DEC_THREADS);
-    *abort_flag = 0;
-    ptx::fence_mbar_init();
-  }
   if (warp == 1) {
     ptx::tmem_alloc(tmem_slot, C::TMEM_COLS);
     ptx::tmem_relinquish();
@@ -642,12 +642,14 @@ constexpr int CMB_WARPS = 4;
 template <int NG, bool WIN>
 __global__ void __launch_bounds__(CMB_WARPS * 32) decode_combine_kernel(const DecArgs p, int G) {
   __shared__ int pre[260];
-  // WIN: waits first, as the attention kernel does (all rows of a padded batch may be empty); otherwise the
-  // plan, which comes from pos alone, is formed beside the attention's end.
-  if (WIN) ptx::griddep_wait();
+  // The plan comes from pos alone, which is complete, as the attention kernel lets this one start only after
+  // a wait of its own or behind one; it is formed beside the attention's end.
   ptx::griddep_launch_dependents();
   if (WIN) decode_window_prefix(p.win, p.pos, p.B, pre);
   else decode_tile_prefix(p.pos, p.B, p.L_max, pre);
+  // WIN: every thread waits, before the returns below too: all rows of a padded batch may be empty, and whoever
+  // waits for this grid has to be behind the kernels before it.
+  if (WIN) ptx::griddep_wait();
   if (blockIdx.x == 0)
     for (int z = threadIdx.x; z < p.n_zero; z += blockDim.x) p.zero_cnt[z] = 0;  // the next kernel's counters
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
