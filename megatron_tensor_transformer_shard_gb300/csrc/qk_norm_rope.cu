@@ -334,6 +334,7 @@ __global__ void __launch_bounds__(THREADS, 2) qk_norm_rope_append_kernel(const Q
 // version 720 us for both.  96 heads x 2048: both 131 us (81 % of the copy rate).
 constexpr int STREAM_WARPS = 12, STREAM_THREADS = STREAM_WARPS * 32, STREAM_RING = 3;
 constexpr int WARP_EXTRA = 2 * (HD / 2) * 4 + 64;  // cosines, sines, ring barriers
+constexpr size_t SUMS_BYTES = 2 * STREAM_WARPS * 2 * HD * sizeof(float);  // dgamma of two groups a warp
 enum : int { ERR_QKNR_STREAM = 0x161 };
 
 // Position in the unit order of one warp.
@@ -571,7 +572,7 @@ __global__ void __launch_bounds__(STREAM_THREADS, 1) qk_norm_rope_stream_kernel(
     // groups are added in order, the CTAs' sums in CTA order by the next kernel, so the result does
     // not depend on timing.
     __syncthreads();  // the rings are done with
-    float* sums = reinterpret_cast<float*>(smem);  // [32 groups][2][128]
+    float* sums = reinterpret_cast<float*>(smem);  // SUMS_BYTES: [24 groups][2][128]
     const int group = warp * 2 + grp;
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {
@@ -624,15 +625,15 @@ __global__ void __launch_bounds__(FIN_COLS * FIN_ROWS)
   }
 }
 
-// CTAs for `units` group visits, at most `per_sm` a multiprocessor (all resident at once).
+// CTAs for `units` group visits, at most `per_sm` for each multiprocessor.
 unsigned grid_for(int64_t units, int per_sm) {
   const int64_t want = (units + GROUPS - 1) / GROUPS;
   const int64_t most = static_cast<int64_t>(device_sm_count()) * per_sm;
   return static_cast<unsigned>(want < most ? (want > 0 ? want : 1) : most);
 }
 
-// Heads per group visit: all of a row's share the token's sines and cosines; few rows are cut finer,
-// so that the GPU's groups (SMs x 4 CTAs x 16) all get work.
+// Heads per group visit: all of a row's share the token's sines and cosines; few rows are cut finer, into
+// at least 4 CTAs of 16 groups for each SM (two fit at a time).
 void set_chunks(QkArgs& a) {
   const int64_t fill = static_cast<int64_t>(device_sm_count()) * 4 * GROUPS;
   int64_t chunks = (fill + a.rows - 1) / a.rows;
@@ -678,9 +679,9 @@ template <bool BWD, bool BF16, bool GBF16, int ROT, bool NORM>
 tp_status launch_stream(const QkArgs& a, unsigned grid, cudaStream_t s) {
   auto kernel = qk_norm_rope_stream_kernel<BWD, BF16, GBF16, ROT, NORM>;
   const int slot = a.hpg * HD * 2 * (BWD && NORM ? 2 : 1);
-  // the backward's last sums take 32 KB of the rings' room
+  // the backward's last sums take the rings' room
   const size_t rings = static_cast<size_t>(STREAM_WARPS) * (STREAM_RING * slot + WARP_EXTRA);
-  const size_t smem = BWD && NORM && rings < 32768 ? 32768 : rings;
+  const size_t smem = BWD && NORM && rings < SUMS_BYTES ? SUMS_BYTES : rings;
   static bool configured[64] = {};
   int dev = 0;
   TP_CUDA_CHECK(cudaGetDevice(&dev));
