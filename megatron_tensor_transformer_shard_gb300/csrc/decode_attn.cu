@@ -212,8 +212,8 @@ __device__ __forceinline__ void softmax_bar() {
 
 // WIN: sliding window with sink tokens.  The tile list then comes from decode_runs(), a tile's keys
 // start at its run, and sequences may have no tiles; all else is the same.  Measured, 64 / 8 heads: 32
-// sequences with 4100 visible keys of 8192 90 us, 256 rolling caches of 1028 179 us (6.0 and 6.1 TB/s,
-// 90 and 91 % of the copy rate).
+// sequences with 4100 visible keys of 8192 93 us, 256 rolling caches of 1028 179 us (5.8 and 6.1 TB/s,
+// 87 and 91 % of the copy rate).
 template <int NG, int GSZ, bool WIN>
 __global__ void __launch_bounds__(DEC_THREADS, 1)
     decode_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,

@@ -17,7 +17,7 @@
 // lanes and four angles a lane.  (With 8 consecutive columns a lane the partner half came by
 // shuffles, with eight angles a lane and a selection between query and key factors per element:
 // 1330 us for 32768 tokens, 64 / 8 heads, forward and backward, against 720; the copies through
-// shared memory below bring that to 568.)  A token's sines and cosines are formed once and
+// shared memory below bring that to 563.)  A token's sines and cosines are formed once and
 // multiplied by gamma once for the query heads and once for the key heads.  Arithmetic is
 // packed, two fp32 an instruction.
 //
@@ -329,9 +329,9 @@ __global__ void __launch_bounds__(THREADS, 2) qk_norm_rope_append_kernel(const Q
 // slot, one load ahead.  No barrier between warps.  Units run token-major (token, shard, run of
 // heads), each warp over a contiguous range of them, so the sines and cosines of a token are
 // formed once for all its shards' heads, by all 32 lanes, and wait in shared memory.
-// Measured (N 32768, 64 / 8 heads, t 8, norm + rotation): forward 220 us = 6.1 TB/s, 91 % of the
-// copy rate; backward 354 us = 5.5 TB/s of dY, X, dX (8 issue slots of 10 taken); the register
-// version 720 us for both.  96 heads x 2048: both 131 us (81 % of the copy rate).
+// Measured (N 32768, 64 / 8 heads, t 8, norm + rotation): forward 238 us = 5.6 TB/s, 85 % of the
+// copy rate; backward 335 us = 5.8 TB/s of dY, X, dX, 87 % (55 % of the issue slots taken); both, one
+// after the other, 563 us; the register version 720.  96 heads x 2048: both 121 us (87 % of the copy rate).
 constexpr int STREAM_WARPS = 12, STREAM_THREADS = STREAM_WARPS * 32, STREAM_RING = 3;
 constexpr int WARP_EXTRA = 2 * (HD / 2) * 4 + 64;  // cosines, sines, ring barriers
 constexpr size_t SUMS_BYTES = 2 * STREAM_WARPS * 2 * HD * sizeof(float);  // dgamma of two groups a warp

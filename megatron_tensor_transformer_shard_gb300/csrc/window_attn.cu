@@ -35,10 +35,9 @@
 // as long as the tensor cores take to run it, and its pauses were theirs (N 16384, 64 / 8 heads, W 1024,
 // seven sequences, forward and backward: 2296 us, elected 1857).
 //
-// Measured, 64 / 8 heads, N 16384: forward W 1024, 16 sinks 465 us (1163 TFLOP/s of visible pairs; the
+// Measured, 64 / 8 heads, N 16384: forward W 1024, 16 sinks 466 us (1163 TFLOP/s of visible pairs; the
 // 128-key blocks at the two edges and the sinks' make it 10 blocks where 8 would hold the window), full
-// causal 2535 us (1735); dQ 698 us, dK / dV 830 us at W 1024 (SM throughput 77 and 88 %, the longest CTA
-// of dK / dV 96 %).
+// causal 2560 us (1718); dQ 703 us, dK / dV 842 us at W 1024 (SM throughput 79 and 85 %).
 //
 // P and dS are rounded to fp16 (2^-11, relative) because the MMA takes 16-bit operands; scores, row
 // maxima and sums, lse, D and every accumulator stay fp32.  Near zero fp16 has 2^-25 absolute.  Against
