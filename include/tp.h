@@ -602,7 +602,8 @@ typedef struct tp_attn_options {
  * the required part (the window's, with cu_seqlens only), then room for the GEMMs' split K.
  * Backward: tp_attn_gqa_backward with the same `opt`; QKV_raw is required with norms.
  * dq_gamma, dk_gamma [128] fp32 (nullable; only with norms) follow `accumulate`.  X and dY in
- * rows of no sequence must be finite; dQKV is 0 there, and dO is not used.  ws:
+ * rows of no sequence must be finite (with norms, X's projection within fp16 too); dQKV is 0
+ * there, and dO is not used.  ws:
  * tp_attn_opt_backward_workspace_size() bytes, 256-byte aligned, over none of the inputs or dX
  * (TP_ERR_INVALID_ARG).  What the operators between the projections refuse is refused before
  * anything is launched. */
