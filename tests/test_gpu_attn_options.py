@@ -232,3 +232,35 @@ def test_padding_of_zeros_leaves_the_gradients_alone():
         assert torch.isfinite(a[k]).all()
         assert_close(k, f64(a[k]), f64(b[k]), 1e-5)
     assert_close("dX", f64(a["dX"][:n]), f64(b["dX"]))
+
+
+def test_block_in_a_replayed_graph():
+    """Forward and backward of the block captured once, replayed with other rows, positions and boundaries."""
+    n_heads, n_kv, t, N = 8, 2, 2, 300
+    inp = I.gqa_attn_inputs(N, 1024, n_heads, n_kv, 128, seed=3)
+    dev = {k: v.cuda() for k, v in inp.items()}
+    w = T.DecodeAttnWeights(dev["W_qkv"], dev["b_qkv"], dev["W_o"], dev["b_o"], n_heads, n_kv, 128, t)
+    opt, _ = options(True, 128, 48, 3, [0, 100, 300], np.arange(N))
+    X, dY = dev["X"].clone(), dev["dY"].clone()
+
+    def both():
+        out = T.attn_opt_forward(X, w.Wqkv_p, w.bqkv_p, w.Wo_p, w.b_o, n_heads, n_kv, t, opt)
+        g = T.attn_opt_backward(dY, X, *out[1:], w.Wqkv_p, w.Wo_p, n_heads, n_kv, t, opt)
+        return [out[0], *g.values()]
+    both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both()
+    for seed, cu in ((1, [0, 7, 300]), (2, [0, 200, 257]), (3, [0, 0, 1])):
+        g = torch.Generator().manual_seed(seed)
+        X.copy_(torch.randn(N, 1024, generator=g))
+        dY.copy_(2.0 ** -8 * seed * torch.randn(N, 1024, generator=g))
+        opt.cu_seqlens.copy_(torch.tensor(cu, dtype=torch.int32))
+        opt.pos.add_(1000)
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = [x.clone() for x in got]
+        for a, b in zip(kept, both()):
+            assert torch.equal(a, b)
+    assert L.tp_get_device_status(check=False) == L.TP_OK

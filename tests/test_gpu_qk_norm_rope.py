@@ -358,3 +358,20 @@ def test_gamma_gradients_within_the_longest_chain(n_heads, n_kv, t, N):
     units = gamma_units(t, N, n_heads, n_kv)
     within(got[1], dq, units * bq)
     within(got[2], dk, units * bk)
+
+
+@pytest.mark.parametrize("n_heads,n_kv,t,N", [(200, 1, 1, 3), (96, 96, 1, 70), (130, 65, 1, 1)])
+def test_many_heads_a_shard(n_heads, n_kv, t, N):
+    X = rnd(1, t, N, width(n_heads, n_kv, t))
+    G = rnd(5, *X.shape, dtype=torch.bfloat16)
+    gq, gk = gammas(2, True)
+    f = T.rope_frequencies(64, device="cpu")
+    ref, tol = O.qk_norm_rope(f64(X), n_heads, n_kv, f64(gq), f64(gk), 1e-6, f.numpy())
+    args = (n_heads, n_kv, *cuda(gq, gk), 1e-6, f.cuda())
+    within(T.qk_norm_rope_forward(X.cuda(), *args), ref, tol)
+    dX, dq, dk, bX, bq, bk = O.qk_norm_rope_backward(f64(G), f64(X), n_heads, n_kv, f64(gq), f64(gk), 1e-6, f.numpy())
+    got = T.qk_norm_rope_backward(G.cuda(), X.cuda(), *args)
+    within(got[0], dX, 2.0 ** -8 * np.abs(dX) + 84 * 2.0 ** -24 * bX)
+    units = gamma_units(t, N, n_heads, n_kv)
+    within(got[1], dq, units * bq)
+    within(got[2], dk, units * bk)
